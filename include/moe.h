@@ -281,6 +281,38 @@ int moe_profile_set_events(void *const *events, int n);
 unsigned long long moe_launch_count(void);
 
 /* ------------------------------------------------------------------------- *
+ * Products grouped by expert, with gradients.
+ *
+ * The linear maps of an expert layer, one call each, for programs that train the
+ * experts or put the layer together themselves (the page "GLM-4.5 MoE Forward",
+ * How it works, uses two: gate_up_proj and down_proj).  The rows are sorted by
+ * expert: row r belongs to expert e when offsets[e] <= r < offsets[e+1].
+ * Segments may be empty and of any length; nothing is padded.
+ *
+ *   moe_grouped_linear         y_r = W_e x_r
+ *   moe_grouped_linear_dgrad   dx_r = W_e^T dy_r
+ *   moe_grouped_linear_wgrad   dW_e = sum over e's rows of dy_r x_r^T (zeros for an
+ *                              expert without rows; dW is fully overwritten)
+ *
+ *   x, dx   [rows, K]   dtype      y, dy   [rows, M]   dtype
+ *   W, dW   [E, M, K]   dtype      offsets [E+1]       int32, device, 4-byte aligned
+ * dtype MOE_BF16: tensor cores, fp32 accumulation, one rounding; M and K multiples
+ * of 8.  MOE_F32: CUDA cores, fp32 sums in index order; M and K multiples of 4.
+ * 1 <= E <= 512.  No workspace; results are bitwise reproducible.
+ * Rows of no expert (before offsets[0], from offsets[E] on) are not read; in y and
+ * dx they are left as they were, or written zero if zero_rest is not 0.
+ * Offsets are clamped to [0, rows] and to be non-decreasing; if that changes any,
+ * moe_device_status() reports MOE_ERR_BAD_INDEX.  rows = 0 is a no-op, but for
+ * dW, which is zeroed.  Outputs must not overlap inputs.
+ */
+int moe_grouped_linear(const void *x, const void *W, const int32_t *offsets, int rows, int E, int M,
+                       int K, int dtype, void *y, int zero_rest, void *stream);
+int moe_grouped_linear_dgrad(const void *dy, const void *W, const int32_t *offsets, int rows, int E,
+                             int M, int K, int dtype, void *dx, int zero_rest, void *stream);
+int moe_grouped_linear_wgrad(const void *dy, const void *x, const int32_t *offsets, int rows, int E,
+                             int M, int K, int dtype, void *dW, void *stream);
+
+/* ------------------------------------------------------------------------- *
  * Expert parallelism over peer memory.
  *
  * "GLM-5.3-Flash Module 02" (expert placement and popularity) treats the

@@ -7,6 +7,8 @@ no fallback: if libmoe.so is missing or no sm_100 GPU is current, calls raise.
 
     idx, w = moe_router(x, W_g, b, n_group, topk_group, k, norm_topk_prob, alpha)
     y = moe_forward(x, gate_up, down, sh_gate, sh_up, sh_down, idx, w)
+
+The experts' products by themselves, with gradients, are in products.py.
 """
 
 from __future__ import annotations
@@ -26,7 +28,8 @@ __all__ = ["MoEError", "moe_router", "moe_forward", "moe_forward_workspace", "mo
            "EXPORTED_SYMBOLS", "moe_ep_symmetric_bytes", "moe_ep_workspace_bytes",
            "moe_ep_forward", "moe_ep_plan_host", "moe_ep_ipc_export", "moe_ep_ipc_open",
            "moe_ep_ipc_close", "ExpertParallelGroup", "MOE_EP_COUNT", "MOE_EP_SEND",
-           "MOE_EP_EXPERTS", "MOE_EP_COMBINE", "MOE_EP_ALL", "moe_bias_update"]
+           "MOE_EP_EXPERTS", "MOE_EP_COMBINE", "MOE_EP_ALL", "moe_bias_update",
+           "moe_grouped_linear", "moe_grouped_linear_dgrad", "moe_grouped_linear_wgrad"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libmoe.so")
@@ -45,7 +48,8 @@ EXPORTED_SYMBOLS = ("moe_router", "moe_forward_workspace", "moe_layer_forward_wo
                     "moe_status_string", "moe_version", "moe_debug_set_wait_limit_ns",
                     "moe_debug_never_signal", "moe_profile_set_events", "moe_launch_count",
                     "moe_debug_capture_scores", "moe_debug_set_pair_mode", "moe_forward_noalloc", "moe_forward_clamped", "moe_layer_forward",
-                    "moe_bias_update",
+                    "moe_bias_update", "moe_grouped_linear", "moe_grouped_linear_dgrad",
+                    "moe_grouped_linear_wgrad",
                     "moe_ep_symmetric_bytes",
                     "moe_ep_workspace_bytes", "moe_ep_forward", "moe_ep_plan_host",
                     "moe_ep_ipc_export", "moe_ep_ipc_open", "moe_ep_ipc_close")
@@ -110,6 +114,10 @@ def load_library():
         lib.moe_layer_forward.restype = I
         lib.moe_bias_update.argtypes = [P, I, I, I, F, P, P, P]
         lib.moe_bias_update.restype = I
+        for f in (lib.moe_grouped_linear, lib.moe_grouped_linear_dgrad):
+            f.argtypes, f.restype = [P, P, P, I, I, I, I, I, P, I, P], I
+        lib.moe_grouped_linear_wgrad.argtypes = [P, P, P, I, I, I, I, I, P, P]
+        lib.moe_grouped_linear_wgrad.restype = I
         lib.moe_ep_symmetric_bytes.argtypes = [I, I, I, I, I]
         lib.moe_ep_symmetric_bytes.restype = S
         lib.moe_ep_workspace_bytes.argtypes = [I, I, I, I, I, I, I]
@@ -476,3 +484,7 @@ class ExpertParallelGroup:
         for ptr in self._opened:
             moe_ep_ipc_close(ptr)
         self._opened = []
+
+
+from .products import (moe_grouped_linear, moe_grouped_linear_dgrad,  # noqa: E402
+                       moe_grouped_linear_wgrad)

@@ -1,0 +1,528 @@
+// Matrix products grouped by expert over ragged row segments, with both gradients.
+// Row r in [off[e], off[e+1]) belongs to expert e; W is [E, M, K]:
+//
+//   forward  y_r  = W_e x_r                     rows x M,  sums over K
+//   dgrad    dx_r = W_e^T dy_r                  rows x K,  sums over M
+//   wgrad    dW_e = sum over e's rows dy_r x_r^T  M x K,   sums over the rows
+//
+// The segments are used where they lie: no permuted or padded copy.  A TMA box may
+// start at any row, so a tile's 128 rows begin at the segment's own row.  Rows of a
+// box past the segment's end belong to other experts: in forward and dgrad they
+// only fill output rows that are not stored; in wgrad they would enter the sum,
+// so the last k-block is cut to the 16 rows an MMA step takes and the rows past the
+// end are zeroed in shared memory, in both operands (a NaN there must not meet a 0).
+//
+// bf16: tcgen05.mma, 128 x 256 output tiles, k-blocks of 64, fp32 accumulators in
+// TMEM, one rounding to bf16.  Persistent, one CTA per SM, warp-specialised like the
+// forward's GEMMs: warp 0 TMA, warp 1 MMA, warps 2-5 epilogue; two accumulators.
+// The operands keep their memory layout.  Where the summed index is contiguous the
+// shared-memory tile is K-major (forward both, dgrad dy); where it is the row the
+// tile is MN-major (dgrad W, wgrad both) and the MMA reads it transposed.
+#pragma once
+
+#include "common.cuh"
+#include "gemm_sm100.cuh"
+
+namespace moe {
+
+enum GroupedMode { GRP_FORWARD = 0, GRP_DGRAD = 1, GRP_WGRAD = 2 };
+
+constexpr int GRP_BM = 128;
+constexpr int GRP_BN = 256;
+constexpr int GRP_BK = 64;
+constexpr int GRP_STAGES = 4;
+constexpr int GRP_THREADS = 192;
+constexpr int GRP_MAXE = 512;
+constexpr int GRP_A_BYTES = GRP_BM * GRP_BK * 2; // 16 KiB
+constexpr int GRP_B_BYTES = GRP_BN * GRP_BK * 2; // 32 KiB
+constexpr int GRP_STAGE_BYTES = GRP_A_BYTES + GRP_B_BYTES;
+constexpr int GRP_CHUNK = 64 * 64 * 2; // an MN-major box: 64 rows of 64 elements
+constexpr int GRP_OUT_BUF = 32 * 32 * 2;
+constexpr int GRP_TAB_OFF = GRP_STAGES * GRP_STAGE_BYTES + 256;
+constexpr int GRP_STG_OFF = (GRP_TAB_OFF + 2 * (GRP_MAXE + 1) * 4 + 1023) / 1024 * 1024;
+constexpr int GRP_SMEM_BYTES = 1024 + GRP_STG_OFF + 4 * 2 * GRP_OUT_BUF;
+static_assert(GRP_SMEM_BYTES <= 232448, "shared memory");
+static_assert((2 * GRP_STAGES + 5) * 8 + 8 <= 256, "barrier block");
+
+struct GroupedArgs {
+    const int32_t *offsets; // [E+1]
+    int rows, E;
+    int M, K;     // W is [E, M, K]
+    int red;      // forward K, dgrad M (wgrad: the segment's rows)
+    int ncols;    // output columns: forward M, dgrad K, wgrad K
+    int nb;       // output column blocks
+    int mb;       // wgrad: output row blocks
+    void *out;
+    int zero_rest; // forward, dgrad: write zeros to the rows of no expert
+    uint64_t wait_limit_ns;
+};
+
+// Shared-memory matrix descriptor of an MN-major tile written by TMA with 128-byte
+// swizzle: rows of the summed index, 128 bytes (64 elements of M or N) each; eight
+// rows are 1024 bytes (stride byte offset), the next 64 elements of M or N are one
+// box further (leading byte offset).
+__device__ __forceinline__ uint64_t umma_desc_sw128_mn(uint32_t saddr, uint32_t box_bytes) {
+    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(box_bytes >> 4) << 16) |
+           ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+// Instruction descriptor bits: the operand is MN-major (transposed).
+constexpr uint32_t UMMA_A_MN = 1u << 15;
+constexpr uint32_t UMMA_B_MN = 1u << 16;
+
+__device__ __forceinline__ void tma_load_3d(const CUtensorMap *map, uint64_t *bar, void *dst,
+                                            int c0, int c1, int c2) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
+        : "memory");
+}
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, const void *src, int c0, int c1,
+                                             int c2) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(smem_u32(src)), "r"(c0), "r"(c1), "r"(c2)
+                 : "memory");
+}
+
+// The segment table: s_off[0..E] the offsets, made safe (within [0, rows] and not
+// decreasing; what was not is reported by one CTA), and s_tile[0..E] the prefix of
+// row tiles of `tile` rows.  One warp; lanes take consecutive experts.
+__device__ __forceinline__ void grouped_table(const int32_t *offsets, int E, int rows, int tile,
+                                              int *s_off, int *s_tile, bool report, int lane) {
+    int top = 0; // running maximum of the offsets
+    bool bad = false;
+    for (int base = 0; base <= E; base += 32) {
+        const int i = base + lane;
+        const int raw = i <= E ? offsets[i] : rows;
+        int v = min(max(raw, 0), rows);
+        bad |= v != raw;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int n = __shfl_up_sync(0xffffffffu, v, d);
+            if (lane >= d) v = max(v, n);
+        }
+        v = max(v, top);
+        bad |= i <= E && v != raw;
+        if (i <= E) s_off[i] = v;
+        top = __shfl_sync(0xffffffffu, v, 31);
+    }
+    if (report && __any_sync(0xffffffffu, bad) && lane == 0) record_error(DEV_BAD_INDEX, 300);
+    __syncwarp();
+    int carry = 0;
+    for (int base = 0; base <= E; base += 32) {
+        const int e = base + lane;
+        const int v = e < E ? (s_off[e + 1] - s_off[e] + tile - 1) / tile : 0;
+        int incl = v;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int n = __shfl_up_sync(0xffffffffu, incl, d);
+            if (lane >= d) incl += n;
+        }
+        if (e <= E) s_tile[e] = carry + incl - v;
+        carry += __shfl_sync(0xffffffffu, incl, 31);
+    }
+}
+
+// Zeros to the rows outside [lo, hi): threads tid, tid + step, ... of 16-byte pieces.
+__device__ __forceinline__ void grouped_zero_rest(void *out, int rows, size_t row_bytes, int lo, int hi,
+                                                  size_t tid, size_t step) {
+    const size_t per = row_bytes >> 4;
+    const size_t head = (size_t)lo * per, n = head + (size_t)(rows - hi) * per;
+    uint4 *p = static_cast<uint4 *>(out);
+    for (size_t i = tid; i < n; i += step)
+        p[i < head ? i : (size_t)hi * per + (i - head)] = make_uint4(0u, 0u, 0u, 0u);
+}
+
+struct GroupedTile {
+    int e;
+    int r0, r1; // forward, dgrad: output rows [r0, r1); wgrad: summed rows [r0, r1)
+    int m0;     // wgrad: first output row
+    int n0;     // first output column
+    int kb;     // k-blocks
+};
+
+template <int MODE>
+__device__ __forceinline__ GroupedTile grouped_tile(int t, const GroupedArgs &a, const int *s_off,
+                                                    const int *s_tile) {
+    GroupedTile c;
+    if (MODE == GRP_WGRAD) {
+        const int per = a.nb * a.mb;
+        c.e = t / per;
+        const int l = t - c.e * per;
+        const int n = l / a.mb;
+        c.n0 = n * GRP_BN;
+        c.m0 = (l - n * a.mb) * GRP_BM;
+        c.r0 = s_off[c.e];
+        c.r1 = s_off[c.e + 1];
+        c.kb = (c.r1 - c.r0 + GRP_BK - 1) / GRP_BK;
+    } else {
+        // Expert by expert, column block by column block: the row tiles that read the
+        // same weight tile are neighbours and run at the same time.
+        c.e = find_expert(s_tile, a.E, a.nb, t);
+        const int mt = s_tile[c.e + 1] - s_tile[c.e];
+        const int l = t - s_tile[c.e] * a.nb;
+        const int n = l / mt;
+        c.n0 = n * GRP_BN;
+        c.m0 = 0;
+        c.r0 = s_off[c.e] + (l - n * mt) * GRP_BM;
+        c.r1 = min(c.r0 + GRP_BM, s_off[c.e + 1]);
+        c.kb = (a.red + GRP_BK - 1) / GRP_BK;
+    }
+    return c;
+}
+
+// Maps.  forward: mA x [rows, K] box 64 x 128 rows, mB W [E, M, K] box 64 x 256 x 1,
+// mOut y [rows, M] box 32 x 32.  dgrad: mA dy [rows, M] box 64 x 128, mB W box
+// 64 x 64 x 1, mOut dx [rows, K].  wgrad: mA dy box 64 x 64, mB x [rows, K] box
+// 64 x 64, mOut dW [E, M, K] box 32 x 32 x 1.
+template <int MODE>
+__global__ void __launch_bounds__(GRP_THREADS, 1)
+    grouped_product_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtensorMap mB,
+                           const __grid_constant__ CUtensorMap mOut, const GroupedArgs a) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    uint8_t *ring = smem;
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + GRP_STAGES * GRP_STAGE_BYTES);
+    uint64_t *empty = full + GRP_STAGES;
+    uint64_t *tfull = empty + GRP_STAGES;
+    uint64_t *tempty = tfull + 2;
+    uint64_t *drain = tempty + 2;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    int *s_off = reinterpret_cast<int *>(smem + GRP_TAB_OFF);
+    int *s_tile = s_off + GRP_MAXE + 1;
+
+    const int warp = warp_id(), lane = lane_id();
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < GRP_STAGES; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&tfull[i], 1);
+            mbar_init(&tempty[i], 4);
+        }
+        mbar_init(drain, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+        tma_prefetch_desc(&mA);
+        tma_prefetch_desc(&mB);
+        tma_prefetch_desc(&mOut);
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_slot, 512);
+        tmem_relinquish();
+    }
+    if (warp == 2)
+        grouped_table(a.offsets, a.E, a.rows, GRP_BM, s_off, s_tile, blockIdx.x == 0, lane);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+    const int total = MODE == GRP_WGRAD ? a.E * a.nb * a.mb : s_tile[a.E] * a.nb;
+    const uint64_t limit = a.wait_limit_ns;
+
+    if (warp == 0) {
+        // ------------------------------ TMA producer ------------------------------
+        if (lane == 0) {
+            uint32_t it = 0;
+            bool ok = true;
+            for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+                const GroupedTile c = grouped_tile<MODE>(t, a, s_off, s_tile);
+                // Column blocks of one row tile start at different k-blocks, so they do
+                // not all ask for the same rows at once.  (wgrad keeps the order: its
+                // last k-block is the one that is cut.)
+                const int rot = MODE == GRP_WGRAD ? 0 : (c.n0 / GRP_BN) % c.kb;
+                for (int i = 0; i < c.kb; ++i, ++it) {
+                    const int kb = i + rot < c.kb ? i + rot : i + rot - c.kb;
+                    const uint32_t s = it % GRP_STAGES, ph = (it / GRP_STAGES) & 1;
+                    if (!mbar_wait(&empty[s], ph ^ 1, limit, abort_flag, 301)) { ok = false; break; }
+                    uint8_t *sa = ring + s * GRP_STAGE_BYTES, *sb = sa + GRP_A_BYTES;
+                    mbar_arrive_expect_tx(&full[s], GRP_STAGE_BYTES);
+                    const int kx = kb * GRP_BK;
+                    if (MODE == GRP_FORWARD) {
+                        tma_load_2d(&mA, &full[s], sa, kx, c.r0);
+                        tma_load_3d(&mB, &full[s], sb, kx, c.n0, c.e);
+                    } else if (MODE == GRP_DGRAD) {
+                        tma_load_2d(&mA, &full[s], sa, kx, c.r0);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            tma_load_3d(&mB, &full[s], sb + j * GRP_CHUNK, c.n0 + 64 * j, kx, c.e);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 2; ++j)
+                            tma_load_2d(&mA, &full[s], sa + j * GRP_CHUNK, c.m0 + 64 * j, c.r0 + kx);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            tma_load_2d(&mB, &full[s], sb + j * GRP_CHUNK, c.n0 + 64 * j, c.r0 + kx);
+                    }
+                }
+            }
+            if (!ok) {
+                // Let copies already issued land before the CTA's memory goes away.
+                const uint32_t first = it > GRP_STAGES ? it - GRP_STAGES : 0;
+                for (uint32_t j = first; j < it; ++j) {
+                    volatile int no_abort = 0;
+                    mbar_wait(&full[j % GRP_STAGES], (j / GRP_STAGES) & 1, 10000000ull, &no_abort, 302);
+                }
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ------------------------------ MMA issuer --------------------------------
+        // The whole warp walks the loop (it zeroes the rows past a segment's end);
+        // lane 0 waits and issues.
+        uint32_t it = 0, tc = 0;
+        bool ok = true;
+        for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+            const GroupedTile c = grouped_tile<MODE>(t, a, s_off, s_tile);
+            if (c.kb == 0) continue; // wgrad of an expert without rows: zeros
+            const uint32_t acc = tc & 1, aph = (tc >> 1) & 1;
+            ++tc;
+            // only the columns that exist, in steps of 16
+            const int n = min(GRP_BN, (a.ncols - c.n0 + 15) & ~15);
+            const uint32_t idesc = umma_idesc_bf16(GRP_BM, n) | (MODE == GRP_WGRAD ? UMMA_A_MN : 0u) |
+                                   (MODE != GRP_FORWARD ? UMMA_B_MN : 0u);
+            if (lane == 0) ok = mbar_wait(&tempty[acc], aph ^ 1, limit, abort_flag, 311);
+            ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t d_tmem = tmem_base + acc * GRP_BN;
+            for (int i = 0; i < c.kb; ++i, ++it) {
+                const uint32_t s = it % GRP_STAGES, ph = (it / GRP_STAGES) & 1;
+                if (lane == 0) ok = mbar_wait(&full[s], ph, limit, abort_flag, 312);
+                ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+                if (!ok) break;
+                int steps = GRP_BK / 16;
+                if (MODE == GRP_WGRAD && i == c.kb - 1) {
+                    const int valid = c.r1 - c.r0 - i * GRP_BK; // rows of this k-block, 1..64
+                    steps = (valid + 15) >> 4;
+                    const int pad = steps * 16 - valid;
+                    if (pad) {
+                        uint4 *p = reinterpret_cast<uint4 *>(ring + s * GRP_STAGE_BYTES);
+                        for (int j = lane; j < 6 * 8 * pad; j += 32) {
+                            const int box = j / (8 * pad), o = j - box * 8 * pad;
+                            p[box * (GRP_CHUNK / 16) + valid * 8 + o] = make_uint4(0u, 0u, 0u, 0u);
+                        }
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                    }
+                }
+                if (lane == 0) {
+                    tc_fence_after();
+                    const uint32_t sa = smem_u32(ring + s * GRP_STAGE_BYTES);
+                    const uint32_t sb = sa + GRP_A_BYTES;
+#pragma unroll
+                    for (int kk = 0; kk < GRP_BK / 16; ++kk) {
+                        if (MODE == GRP_WGRAD && kk >= steps) break;
+                        const uint64_t da = MODE == GRP_WGRAD
+                                                ? umma_desc_sw128_mn(sa + kk * 2048, GRP_CHUNK)
+                                                : umma_desc_sw128(sa + kk * 32);
+                        const uint64_t db = MODE != GRP_FORWARD
+                                                ? umma_desc_sw128_mn(sb + kk * 2048, GRP_CHUNK)
+                                                : umma_desc_sw128(sb + kk * 32);
+                        umma_bf16_ss(d_tmem, da, db, idesc, (i > 0 || kk > 0) ? 1u : 0u);
+                    }
+                    umma_commit(&empty[s]);
+                }
+            }
+            if (!ok) break;
+            if (lane == 0) umma_commit(&tfull[acc]);
+        }
+        if (lane == 0) {
+            // Drain: wait until every MMA issued by this thread has completed.
+            umma_commit(drain);
+            volatile int no_abort = 0;
+            mbar_wait(drain, 0, 100000000ull, &no_abort, 313);
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------ epilogue ---------------------------------
+        const int q = warp & 3; // TMEM lane quadrant: output rows q*32 + lane of the tile
+        uint8_t *stg = smem + GRP_STG_OFF + q * 2 * GRP_OUT_BUF;
+        uint32_t nstore = 0, tc = 0;
+        for (int t = blockIdx.x; t < total; t += gridDim.x) {
+            const GroupedTile c = grouped_tile<MODE>(t, a, s_off, s_tile);
+            const bool none = c.kb == 0; // nothing accumulated: zeros
+            const uint32_t acc = tc & 1, aph = (tc >> 1) & 1;
+            bool have = none;
+            if (!none) {
+                ++tc;
+                if (lane == 0) have = mbar_wait(&tfull[acc], aph, limit, abort_flag, 321);
+                have = __shfl_sync(0xffffffffu, have ? 1 : 0, 0) != 0;
+            }
+            __syncwarp();
+            if (!have) continue;
+            tc_fence_after();
+            const uint32_t tbase = tmem_base + acc * GRP_BN + ((uint32_t)(q * 32) << 16);
+            // Rows of this warp: wgrad's past M are clipped by the store's map; in the
+            // other modes a part of 32 rows inside the segment is stored by TMA, a
+            // ragged one by each row's thread.
+            const int first = q * 32;
+            const int rows = MODE == GRP_WGRAD ? a.M - c.m0 - first : c.r1 - c.r0 - first;
+            const bool by_tma = MODE == GRP_WGRAD || rows >= 32;
+#pragma unroll 1
+            for (int ch = 0; ch < GRP_BN / 32; ++ch) {
+                const int col = c.n0 + ch * 32;
+                if (col >= a.ncols || rows <= 0) break;
+                uint32_t v[32];
+                if (none) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] = 0u;
+                } else {
+                    tmem_ld_32x32b_x32(tbase + ch * 32, v);
+                    tmem_ld_wait();
+                }
+                uint32_t pk[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    pk[i] = pack_bf16x2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+                const uint4 u[4] = {make_uint4(pk[0], pk[1], pk[2], pk[3]),
+                                    make_uint4(pk[4], pk[5], pk[6], pk[7]),
+                                    make_uint4(pk[8], pk[9], pk[10], pk[11]),
+                                    make_uint4(pk[12], pk[13], pk[14], pk[15])};
+                if (by_tma) {
+                    uint8_t *buf = stg + (nstore & 1) * GRP_OUT_BUF;
+                    if (lane == 0) bulk_wait_group_read<1>(); // the box staged 2 ago left buf
+                    __syncwarp();
+                    uint4 *dst = reinterpret_cast<uint4 *>(buf + lane * 64);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int p = (j + lane) & 3; // fewer bank conflicts
+                        dst[p] = p == 0 ? u[0] : p == 1 ? u[1] : p == 2 ? u[2] : u[3];
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (MODE == GRP_WGRAD)
+                            tma_store_3d(&mOut, buf, col, c.m0 + first, c.e);
+                        else
+                            tma_store_2d(&mOut, buf, col, c.r0 + first);
+                        bulk_commit_group();
+                    }
+                    ++nstore;
+                } else if (lane < rows) {
+                    uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) +
+                                                           (size_t)(c.r0 + first + lane) * a.ncols + col);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (col + 8 * j < a.ncols) dst[j] = u[j];
+                }
+            }
+            if (!none) {
+                // Release the accumulator.
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&tempty[acc]);
+            }
+        }
+        if (lane == 0) bulk_wait_group<0>(); // stores done
+        if (MODE != GRP_WGRAD && a.zero_rest)
+            grouped_zero_rest(a.out, a.rows, (size_t)a.ncols * 2, s_off[0], s_off[a.E],
+                              (size_t)blockIdx.x * 128 + (threadIdx.x - 64), (size_t)gridDim.x * 128);
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem_base, 512);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// fp32: the same three products on the CUDA cores, T x T output tiles, 16 summed
+// indices at a time in shared memory, 4 x 4 sums a thread (fp32, one running sum in
+// index order).  The summed index never crosses a segment, so nothing is masked but
+// loads.  T = 64 for large batches, 32 for small ones (more tiles for the same SMs).
+// ---------------------------------------------------------------------------
+template <int MODE, int T>
+__global__ void __launch_bounds__((T / 4) * (T / 4)) grouped_f32_kernel(const float *A, const float *B,
+                                                                        const GroupedArgs a) {
+    constexpr int NT = (T / 4) * (T / 4), KB = 16;
+    __shared__ float sA[KB][T + 4], sB[KB][T + 4];
+    __shared__ int s_off[GRP_MAXE + 1], s_tile[GRP_MAXE + 1];
+    const int tid = threadIdx.x;
+    if (tid < 32) grouped_table(a.offsets, a.E, a.rows, T, s_off, s_tile, blockIdx.x == 0, tid);
+    __syncthreads();
+    const int total = MODE == GRP_WGRAD ? a.E * a.nb * a.mb : s_tile[a.E] * a.nb;
+    const int tx = tid % (T / 4), ty = tid / (T / 4);
+    float *out = static_cast<float *>(a.out);
+    for (int t = blockIdx.x; t < total; t += gridDim.x) {
+        int e, i0, i1, n0, r0, red;
+        if (MODE == GRP_WGRAD) {
+            const int per = a.nb * a.mb;
+            e = t / per;
+            const int l = t - e * per;
+            n0 = (l / a.mb) * T;
+            i0 = (l % a.mb) * T;
+            i1 = min(i0 + T, a.M);
+            r0 = s_off[e];
+            red = s_off[e + 1] - r0;
+        } else {
+            e = find_expert(s_tile, a.E, a.nb, t);
+            const int mt = s_tile[e + 1] - s_tile[e], l = t - s_tile[e] * a.nb;
+            n0 = (l / mt) * T;
+            i0 = s_off[e] + (l % mt) * T;
+            i1 = min(i0 + T, s_off[e + 1]);
+            r0 = 0;
+            red = a.red;
+        }
+        const float *We = B + (size_t)e * a.M * a.K; // forward, dgrad
+        float acc[4][4] = {};
+        for (int k0 = 0; k0 < red; k0 += KB) {
+            for (int j = tid; j < KB * T; j += NT) {
+                // A(i, k): forward x[i][k], dgrad dy[i][k]: k contiguous; wgrad dy[r0+k][i]
+                const int k = MODE == GRP_WGRAD ? j / T : j % KB;
+                const int i = MODE == GRP_WGRAD ? j % T : j / KB;
+                float v = 0.f;
+                if (k0 + k < red && i0 + i < i1)
+                    v = MODE == GRP_WGRAD ? A[(size_t)(r0 + k0 + k) * a.M + i0 + i]
+                                          : A[(size_t)(i0 + i) * a.red + k0 + k];
+                sA[k][i] = v;
+            }
+            for (int j = tid; j < KB * T; j += NT) {
+                // B(k, n): forward W[n][k]; dgrad W[k][n]; wgrad x[r0+k][n]
+                const int k = MODE == GRP_FORWARD ? j % KB : j / T;
+                const int n = MODE == GRP_FORWARD ? j / KB : j % T;
+                float v = 0.f;
+                if (k0 + k < red && n0 + n < a.ncols)
+                    v = MODE == GRP_FORWARD ? We[(size_t)(n0 + n) * a.K + k0 + k]
+                        : MODE == GRP_DGRAD ? We[(size_t)(k0 + k) * a.K + n0 + n]
+                                            : B[(size_t)(r0 + k0 + k) * a.K + n0 + n];
+                sB[k][n] = v;
+            }
+            __syncthreads();
+#pragma unroll
+            for (int k = 0; k < KB; ++k) {
+                const float4 x = *reinterpret_cast<const float4 *>(&sA[k][ty * 4]);
+                const float4 w = *reinterpret_cast<const float4 *>(&sB[k][tx * 4]);
+                const float xa[4] = {x.x, x.y, x.z, x.w}, wb[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int n = 0; n < 4; ++n) acc[i][n] = fmaf(xa[i], wb[n], acc[i][n]);
+            }
+            __syncthreads();
+        }
+        const int n = n0 + tx * 4;
+        if (n < a.ncols) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int row = i0 + ty * 4 + i;
+                if (row < i1) {
+                    const size_t at = MODE == GRP_WGRAD ? (size_t)e * a.M + row : (size_t)row;
+                    *reinterpret_cast<float4 *>(out + at * a.ncols + n) =
+                        make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+                }
+            }
+        }
+    }
+    if (MODE != GRP_WGRAD && a.zero_rest)
+        grouped_zero_rest(a.out, a.rows, (size_t)a.ncols * 4, s_off[0], s_off[a.E],
+                          (size_t)blockIdx.x * NT + tid, (size_t)gridDim.x * NT);
+}
+
+}  // namespace moe

@@ -1,0 +1,145 @@
+// Host side of the grouped products (moe_grouped_linear and its two gradients):
+// argument checks, tensor maps, launches.  Part of moe.cu's translation unit.
+#pragma once
+
+#include "grouped.cuh"
+
+namespace moe {
+namespace {
+
+// 3-D bf16 map over [d2, d1, d0] (d0 contiguous), boxes of b0 x b1 x 1 elements;
+// out-of-range elements read as zero and are not written.
+bool make_map3(CUtensorMap *m, const void *base, uint64_t d0, uint64_t d1, uint64_t d2, uint32_t b0,
+               uint32_t b1, bool swizzle) {
+    auto fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[3] = {d0, d1, d2};
+    cuuint64_t strides[2] = {d0 * 2, d0 * d1 * 2};
+    cuuint32_t box[3] = {b0, b1, 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box,
+              estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+              swizzle ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B : CU_TENSOR_MAP_L2_PROMOTION_NONE,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int MODE>
+int launch_grouped(const CUtensorMap &mA, const CUtensorMap &mB, const CUtensorMap &mOut,
+                   const GroupedArgs &a, int grid, cudaStream_t st) {
+    static bool attr_set[kMaxDevices] = {}; // function attributes are set per device
+    const int dev = current_device_index();
+    if (dev < 0) return MOE_ERR_CUDA;
+    {
+        std::lock_guard<std::mutex> lk(g_mu);
+        if (!attr_set[dev]) {
+            if (cudaFuncSetAttribute(grouped_product_kernel<MODE>,
+                                     cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     GRP_SMEM_BYTES) != cudaSuccess)
+                return MOE_ERR_CUDA;
+            attr_set[dev] = true;
+        }
+    }
+    grouped_product_kernel<MODE><<<grid, GRP_THREADS, GRP_SMEM_BYTES, st>>>(mA, mB, mOut, a);
+    return launch_status();
+}
+
+// One product.  A and B: forward x, W; dgrad dy, W; wgrad dy, x.
+template <int MODE>
+int grouped_impl(const void *A, const void *B, const int32_t *offsets, int rows, int E, int M, int K,
+                 int dtype, void *out, int zero_rest, void *stream) {
+    if (dtype != MOE_F32 && dtype != MOE_BF16) return MOE_ERR_DTYPE;
+    const int vec = dtype == MOE_BF16 ? 8 : 4; // 16-byte rows
+    if (rows < 0 || E <= 0 || E > GRP_MAXE || M <= 0 || K <= 0 || M % vec || K % vec)
+        return MOE_ERR_SHAPE;
+    // tile numbers are 32-bit: bound their count at the smallest tile (32 x 32)
+    const size_t most = INT32_MAX / 2;
+    const size_t ncols = MODE == GRP_FORWARD ? M : K;
+    if (M > (1 << 24) || K > (1 << 24) || rows > INT32_MAX - 256 ||
+        ((size_t)rows / 32 + E) * (ncols / 32 + 1) > most ||
+        (size_t)E * ((size_t)M / 32 + 1) * ((size_t)K / 32 + 1) > most)
+        return MOE_ERR_SHAPE;
+    if (rows == 0 && MODE != GRP_WGRAD) return MOE_OK;
+    if (!out || !offsets || (rows > 0 && (!A || !B))) return MOE_ERR_ARG;
+    if (!aligned16(A) || !aligned16(B) || !aligned16(out) ||
+        (reinterpret_cast<uintptr_t>(offsets) & 3u))
+        return MOE_ERR_ARG;
+    DeviceInfo *dev = nullptr;
+    int rc = current_device_info(&dev);
+    if (rc != MOE_OK) return rc;
+    if (dev->major != 10) return MOE_ERR_NO_DEVICE;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (rows == 0) { // no row has a gradient
+        const size_t es = dtype == MOE_BF16 ? 2 : 4;
+        return cudaMemsetAsync(out, 0, (size_t)E * M * K * es, st) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+    }
+    GroupedArgs a = {};
+    a.offsets = offsets;
+    a.rows = rows;
+    a.E = E;
+    a.M = M;
+    a.K = K;
+    a.red = MODE == GRP_FORWARD ? K : M;
+    a.ncols = (int)ncols;
+    a.out = out;
+    a.zero_rest = zero_rest ? 1 : 0;
+    a.wait_limit_ns = g_wait_limit_ns;
+
+    if (dtype == MOE_F32) {
+        // Small batches have too few 64-row tiles for the SMs.
+        const bool small = ((size_t)rows / 64 + 1) * (ncols / 64 + 1) < (size_t)dev->sms;
+        const int T = small ? 32 : 64;
+        a.nb = (a.ncols + T - 1) / T;
+        a.mb = (M + T - 1) / T;
+        const size_t tiles = MODE == GRP_WGRAD ? (size_t)E * a.nb * a.mb
+                                               : ((size_t)rows / T + std::min(rows, E)) * a.nb;
+        const int grid = (int)std::min<size_t>(std::max<size_t>(tiles, 1), (size_t)dev->sms * 8);
+        const float *fa = static_cast<const float *>(A), *fb = static_cast<const float *>(B);
+        if (small)
+            grouped_f32_kernel<MODE, 32><<<grid, 64, 0, st>>>(fa, fb, a);
+        else
+            grouped_f32_kernel<MODE, 64><<<grid, 256, 0, st>>>(fa, fb, a);
+        return launch_status();
+    }
+
+    a.nb = (a.ncols + GRP_BN - 1) / GRP_BN;
+    a.mb = (M + GRP_BM - 1) / GRP_BM;
+    CUtensorMap mA, mB, mOut;
+    bool ok;
+    if (MODE == GRP_FORWARD)
+        ok = make_map(&mA, A, K, rows, K, GRP_BM) && make_map3(&mB, B, K, M, E, 64, GRP_BN, true) &&
+             make_map_out(&mOut, out, M, rows, M);
+    else if (MODE == GRP_DGRAD)
+        ok = make_map(&mA, A, M, rows, M, GRP_BM) && make_map3(&mB, B, K, M, E, 64, 64, true) &&
+             make_map_out(&mOut, out, K, rows, K);
+    else
+        ok = make_map(&mA, A, M, rows, M, 64) && make_map(&mB, B, K, rows, K, 64) &&
+             make_map3(&mOut, out, K, M, E, 32, 32, false);
+    if (!ok) return MOE_ERR_CUDA;
+    const size_t tiles = MODE == GRP_WGRAD ? (size_t)E * a.nb * a.mb
+                                           : ((size_t)rows / GRP_BM + std::min(rows, E)) * a.nb;
+    const int grid = (int)std::min<size_t>(tiles, (size_t)dev->sms);
+    return launch_grouped<MODE>(mA, mB, mOut, a, grid, st);
+}
+
+}  // namespace
+}  // namespace moe
+
+extern "C" {
+
+int moe_grouped_linear(const void *x, const void *W, const int32_t *offsets, int rows, int E, int M,
+                       int K, int dtype, void *y, int zero_rest, void *stream) {
+    return moe::grouped_impl<moe::GRP_FORWARD>(x, W, offsets, rows, E, M, K, dtype, y, zero_rest, stream);
+}
+
+int moe_grouped_linear_dgrad(const void *dy, const void *W, const int32_t *offsets, int rows, int E,
+                             int M, int K, int dtype, void *dx, int zero_rest, void *stream) {
+    return moe::grouped_impl<moe::GRP_DGRAD>(dy, W, offsets, rows, E, M, K, dtype, dx, zero_rest, stream);
+}
+
+int moe_grouped_linear_wgrad(const void *dy, const void *x, const int32_t *offsets, int rows, int E,
+                             int M, int K, int dtype, void *dW, void *stream) {
+    return moe::grouped_impl<moe::GRP_WGRAD>(dy, x, offsets, rows, E, M, K, dtype, dW, 0, stream);
+}
+
+}  // extern "C"

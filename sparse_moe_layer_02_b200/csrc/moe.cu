@@ -86,6 +86,10 @@ std::mutex g_mu;
 int current_device_info(DeviceInfo **out) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return MOE_ERR_CUDA;
+    // Binds the device's context to this thread: a thread that has made no CUDA call
+    // yet (autograd's backward thread) has none, and the tensor maps' driver call
+    // needs one.
+    if (cudaSetDevice(dev) != cudaSuccess) return MOE_ERR_CUDA;
     std::lock_guard<std::mutex> lk(g_mu);
     DeviceInfo &d = g_dev[dev];
     if (!d.ready) {
@@ -1443,3 +1447,5 @@ int moe_ep_ipc_close(void *dev_ptr) {
 }
 
 }  // extern "C"
+
+#include "grouped_host.cuh"

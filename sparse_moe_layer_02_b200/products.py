@@ -1,0 +1,142 @@
+"""Products grouped by expert: the experts' linear maps one by one, with gradients.
+
+    y = moe_grouped_linear(x, W, offsets)          # rows [offsets[e], offsets[e+1]) times W[e]^T
+    dx = moe_grouped_linear_dgrad(dy, W, offsets)
+    dW = moe_grouped_linear_wgrad(dy, x, offsets)
+
+moe_grouped_linear takes part in autograd.  Every call runs on the tensors' own device,
+on that device's current stream unless a stream is given, and needs all tensors there.
+"""
+
+from __future__ import annotations
+
+import contextlib
+
+import torch
+
+from . import _check, _dev, _dt, load_library
+
+__all__ = ["moe_grouped_linear", "moe_grouped_linear_dgrad", "moe_grouped_linear_wgrad"]
+
+
+def _device(first, *others):
+    """The device all tensors are on, as an index."""
+    if not isinstance(first, torch.Tensor) or not first.is_cuda:
+        raise ValueError("the tensors must be CUDA tensors")
+    dev = first.device
+    for t in others:
+        if t.device != dev:
+            raise ValueError("the tensors must be on one device (%s and %s)" % (dev, t.device))
+    return dev.index
+
+
+def _on(dev: int):
+    """Makes dev the current device where it is not."""
+    return contextlib.nullcontext() if dev == torch.cuda.current_device() else torch.cuda.device(dev)
+
+
+def _stream_on(dev: int, stream) -> int:
+    if stream is None:
+        return torch.cuda.current_stream(dev).cuda_stream
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+
+
+def _out(t, shape, dtype, dev, name):
+    """An output the caller gave, checked, or a new one (unset)."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=torch.device("cuda", dev))
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device.index != dev:
+        raise ValueError("%s must be %s %s on the inputs' device" % (name, list(shape), dtype))
+    return t
+
+
+def _same_type(*ts):
+    for t in ts[1:]:
+        if t.dtype != ts[0].dtype:
+            raise ValueError("the tensors must share one dtype")
+
+
+def _check_offsets(offsets, E):
+    if offsets.dtype != torch.int32 or tuple(offsets.shape) != (E + 1,):
+        raise ValueError("offsets must be int32 [E + 1]")
+
+
+def _linear(x, W, offsets, y, stream):
+    if x.dim() != 2 or W.dim() != 3 or W.shape[2] != x.shape[1]:
+        raise ValueError("x must be [rows, K] and W [E, M, K]")
+    dev = _device(x, W, offsets)
+    _same_type(x, W)
+    (rows, K), (E, M, _) = x.shape, W.shape
+    _check_offsets(offsets, E)
+    rest = int(y is None)
+    y = _out(y, (rows, M), x.dtype, dev, "y")
+    with _on(dev):
+        _check(load_library().moe_grouped_linear(
+            _dev(x, "x"), _dev(W, "W"), _dev(offsets, "offsets"), rows, E, M, K, _dt(x),
+            _dev(y, "y"), rest, _stream_on(dev, stream)), "moe_grouped_linear")
+    return y
+
+
+class _GroupedLinear(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, W, offsets, stream):
+        ctx.save_for_backward(x, W, offsets)
+        return _linear(x, W, offsets, None, stream)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy):
+        x, W, offsets = ctx.saved_tensors
+        dy = dy.contiguous()
+        dx = moe_grouped_linear_dgrad(dy, W, offsets) if ctx.needs_input_grad[0] else None
+        dW = moe_grouped_linear_wgrad(dy, x, offsets) if ctx.needs_input_grad[1] else None
+        return dx, dW, None, None
+
+
+def moe_grouped_linear(x, W, offsets, y=None, stream=None):
+    """y [rows, M] with y_r = W[e] x_r for the rows r of expert e, offsets[e] <= r < offsets[e+1].
+
+    x [rows, K] and W [E, M, K] bf16 or fp32, offsets int32 [E + 1], all contiguous on one
+    device.  A y that is given keeps its rows of no expert; a new one has zeros there.
+    Differentiable in x and W when no y and no stream is given (the backward pass runs on
+    the stream autograd gives it; rows of no expert have a zero gradient)."""
+    if y is None and torch.is_grad_enabled() and (x.requires_grad or W.requires_grad):
+        if stream is not None:
+            raise ValueError("stream: not with gradients (use torch.cuda.stream)")
+        return _GroupedLinear.apply(x, W, offsets, None)
+    return _linear(x, W, offsets, y, stream)
+
+
+def moe_grouped_linear_dgrad(dy, W, offsets, dx=None, stream=None):
+    """dx [rows, K] with dx_r = W[e]^T dy_r, the gradient of moe_grouped_linear in x.
+    A dx that is given keeps its rows of no expert; a new one has zeros there."""
+    if dy.dim() != 2 or W.dim() != 3 or W.shape[1] != dy.shape[1]:
+        raise ValueError("dy must be [rows, M] and W [E, M, K]")
+    dev = _device(dy, W, offsets)
+    _same_type(dy, W)
+    rows, (E, M, K) = dy.shape[0], W.shape
+    _check_offsets(offsets, E)
+    rest = int(dx is None)
+    dx = _out(dx, (rows, K), dy.dtype, dev, "dx")
+    with _on(dev):
+        _check(load_library().moe_grouped_linear_dgrad(
+            _dev(dy, "dy"), _dev(W, "W"), _dev(offsets, "offsets"), rows, E, M, K, _dt(dy),
+            _dev(dx, "dx"), rest, _stream_on(dev, stream)), "moe_grouped_linear_dgrad")
+    return dx
+
+
+def moe_grouped_linear_wgrad(dy, x, offsets, dW=None, stream=None):
+    """dW [E, M, K] with dW[e] = sum over e's rows of dy_r x_r^T, the gradient of
+    moe_grouped_linear in W (zeros for an expert without rows)."""
+    if dy.dim() != 2 or x.dim() != 2 or dy.shape[0] != x.shape[0]:
+        raise ValueError("dy must be [rows, M] and x [rows, K]")
+    dev = _device(dy, x, offsets)
+    _same_type(dy, x)
+    (rows, M), K, E = dy.shape, x.shape[1], offsets.shape[0] - 1
+    _check_offsets(offsets, E)
+    dW = _out(dW, (E, M, K), dy.dtype, dev, "dW")
+    with _on(dev):
+        _check(load_library().moe_grouped_linear_wgrad(
+            _dev(dy, "dy"), _dev(x, "x"), _dev(offsets, "offsets"), rows, E, M, K, _dt(dy),
+            _dev(dW, "dW"), _stream_on(dev, stream)), "moe_grouped_linear_wgrad")
+    return dW

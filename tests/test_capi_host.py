@@ -141,3 +141,23 @@ def test_bias_update_rejects_bad_arguments():
     assert lib.moe_bias_update(None, 4, 2, 16, float("nan"), 16, None, None) == -1
     assert lib.moe_bias_update(None, 4, 2, 16, 1e-3, None, None, None) == -1     # null b
     assert lib.moe_bias_update(None, 4, 2, 16, 1e-3, 16, None, None) == -1       # null ids
+
+
+def test_grouped_products_reject_bad_arguments():
+    lib = moe.load_library()
+
+    def call(f, rows=10, E=4, M=16, K=24, dt=1, a=16, b=16, off=16, out=16):
+        args = [a, b, off, rows, E, M, K, dt, out]
+        return f(*args, None) if f is lib.moe_grouped_linear_wgrad else f(*args, 0, None)
+    for f in (lib.moe_grouped_linear, lib.moe_grouped_linear_dgrad, lib.moe_grouped_linear_wgrad):
+        assert call(f, dt=5) == -3
+        assert call(f, M=12) == -2 and call(f, K=20) == -2      # bf16 rows of 16 bytes
+        assert call(f, M=6, dt=0) == -2 and call(f, K=2, dt=0) == -2
+        assert call(f, E=0) == -2 and call(f, E=513) == -2 and call(f, rows=-1) == -2
+        assert call(f, rows=2 ** 31 - 1) == -2                   # tile numbers are 32-bit
+        assert call(f, a=None) == -1 and call(f, b=None) == -1 and call(f, out=None) == -1
+        assert call(f, off=None) == -1 and call(f, off=18) == -1
+        assert call(f, a=8) == -1 and call(f, b=24) == -1 and call(f, out=40) == -1
+    assert call(lib.moe_grouped_linear, rows=0, a=None, out=None) == 0
+    assert call(lib.moe_grouped_linear_dgrad, rows=0, a=None, out=None) == 0
+    assert call(lib.moe_grouped_linear_wgrad, rows=0, a=None, b=None, out=None) == -1

@@ -1,0 +1,229 @@
+"""Products grouped by expert against fp64 (moe_grouped_linear and its gradients).
+
+Tolerances.  A bf16 output is one rounding (half a step, 2^-8 relative) of an fp32 sum
+of exact products.  The tensor core's sum is taken to lose at most one step of 2^-22 of
+the largest partial sum per 16 products, so over n products at most n/16 * 2^-22 of
+S = sum |a b|.  An fp32 output is a chain of n fused multiply-adds: at most n * 2^-24 * S.
+Each element is held to that bound of its own S.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+import sparse_moe_layer_02_b200 as moe
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+def _case(sizes, M, K, dtype, lead=0, spare=0, seed=0):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed)
+    E, rows = len(sizes), lead + sum(sizes) + spare
+    off = torch.tensor([lead] + (lead + np.cumsum(sizes)).tolist(), dtype=torch.int32, device=DEV)
+    mk = lambda *s: torch.randn(s, generator=g, device=DEV).to(dtype)
+    return mk(rows, K), mk(E, M, K), mk(rows, M), off
+
+
+def _check(got, exact, mass, n, dtype):
+    exact, mass = exact.double(), mass.double()
+    if dtype == BF16:
+        tol = exact.abs() * 2.0 ** -8 + mass * (n / 16 + 1) * 2.0 ** -22 * (1 + 2.0 ** -8)
+    else:
+        tol = mass * (n + 1) * 2.0 ** -24
+    bad = ~((got.double() - exact).abs() <= tol)
+    assert not bad.any(), (int(bad.sum()), bad.nonzero()[:4].tolist(),
+                           got[bad][:4].tolist(), exact[bad][:4].tolist())
+
+
+def _oracle(x, W, dy, off):
+    o = off.tolist()
+    y, ym = (torch.zeros(dy.shape, device=DEV, dtype=torch.float64) for _ in range(2))
+    dx, dxm = (torch.zeros(x.shape, device=DEV, dtype=torch.float64) for _ in range(2))
+    dW, dWm = (torch.zeros(W.shape, device=DEV, dtype=torch.float64) for _ in range(2))
+    for e in range(W.shape[0]):
+        r = slice(o[e], o[e + 1])
+        xe, we, de = x[r].double(), W[e].double(), dy[r].double()
+        y[r], ym[r] = xe @ we.t(), xe.abs() @ we.abs().t()
+        dx[r], dxm[r] = de @ we, de.abs() @ we.abs()
+        dW[e], dWm[e] = de.t() @ xe, de.abs().t() @ xe.abs()
+    return (y, ym), (dx, dxm), (dW, dWm)
+
+
+SHAPES = [
+    # sizes, M, K, rows before and behind
+    ([1], 8, 8, 0, 0),
+    ([3, 0, 5, 1], 64, 72, 0, 0),
+    ([128, 256, 64], 256, 128, 0, 0),
+    ([127, 129, 0, 0, 1, 31, 33, 63, 65], 264, 200, 0, 7),
+    ([0, 0, 17], 136, 520, 5, 300),
+    ([300, 16, 15, 48], 1000, 328, 1, 1),
+    ([2] * 40 + [0] * 20 + [1] * 9, 520, 1032, 0, 0),
+    ([700], 384, 64, 0, 0),
+]
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("sizes,M,K,lead,spare", SHAPES)
+def test_products_match_fp64(sizes, M, K, lead, spare, dtype):
+    x, W, dy, off = _case(sizes, M, K, dtype, lead, spare)
+    (y, ym), (dx, dxm), (dW, dWm) = _oracle(x, W, dy, off)
+    _check(moe.moe_grouped_linear(x, W, off), y, ym, K, dtype)
+    _check(moe.moe_grouped_linear_dgrad(dy, W, off), dx, dxm, M, dtype)
+    _check(moe.moe_grouped_linear_wgrad(dy, x, off), dW, dWm, max(sizes), dtype)
+    assert moe.moe_device_status() == 0
+
+
+@pytest.mark.parametrize("dtype,M,K", [(F32, 4, 12), (F32, 100, 36)])
+def test_fp32_rows_of_four(dtype, M, K):
+    x, W, dy, off = _case([5, 0, 40], M, K, dtype)
+    (y, ym), (dx, dxm), (dW, dWm) = _oracle(x, W, dy, off)
+    _check(moe.moe_grouped_linear(x, W, off), y, ym, K, dtype)
+    _check(moe.moe_grouped_linear_dgrad(dy, W, off), dx, dxm, M, dtype)
+    _check(moe.moe_grouped_linear_wgrad(dy, x, off), dW, dWm, 40, dtype)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_rows_of_no_expert_are_neither_read_nor_written(dtype):
+    sizes, lead, spare = [33, 0, 70, 1], 6, 9
+    x, W, dy, off = _case(sizes, 136, 80, dtype, lead, spare)
+    (y, ym), (dx, dxm), (dW, dWm) = _oracle(x, W, dy, off)
+    rest = torch.ones(x.shape[0], dtype=torch.bool, device=DEV)
+    rest[lead:lead + sum(sizes)] = False
+    x[rest] = float("nan")
+    dy[rest] = float("inf")
+    gy = moe.moe_grouped_linear(x, W, off, y=torch.full_like(dy, 7.0))
+    gx = moe.moe_grouped_linear_dgrad(dy, W, off, dx=torch.full_like(x, 7.0))
+    assert (gy[rest] == 7.0).all() and (gx[rest] == 7.0).all()
+    _check(gy[~rest], y[~rest], ym[~rest], 80, dtype)
+    _check(gx[~rest], dx[~rest], dxm[~rest], 136, dtype)
+    _check(moe.moe_grouped_linear_wgrad(dy, x, off, dW=torch.full_like(W, float("nan"))), dW, dWm,
+           max(sizes), dtype)
+    assert (moe.moe_grouped_linear(x, W, off)[rest] == 0).all()
+    assert (moe.moe_grouped_linear_dgrad(dy, W, off)[rest] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_one_experts_nan_stays_its_own(dtype):
+    """A NaN or infinity in one expert's rows or weights reaches no other expert's results,
+    though the tiles of neighbours overlap it."""
+    sizes, M, K = [5, 40, 3], 72, 88
+    x, W, dy, off = _case(sizes, M, K, dtype)
+    (y, ym), (dx, dxm), (dW, dWm) = _oracle(x, W, dy, off)
+    x[5:45], dy[5:45], W[1] = float("nan"), float("inf"), float("nan")
+    keep = torch.ones(48, dtype=torch.bool, device=DEV)
+    keep[5:45] = False
+    _check(moe.moe_grouped_linear(x, W, off)[keep], y[keep], ym[keep], K, dtype)
+    _check(moe.moe_grouped_linear_dgrad(dy, W, off)[keep], dx[keep], dxm[keep], M, dtype)
+    got = moe.moe_grouped_linear_wgrad(dy, x, off)
+    for e in (0, 2):
+        _check(got[e], dW[e], dWm[e], 5, dtype)
+    assert torch.isnan(got[1]).all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_no_rows(dtype):
+    x, W, dy, off = _case([0, 0], 16, 24, dtype)
+    assert moe.moe_grouped_linear(x, W, off).shape == (0, 16)
+    assert moe.moe_grouped_linear_dgrad(dy, W, off).shape == (0, 24)
+    assert (moe.moe_grouped_linear_wgrad(dy, x, off, dW=torch.ones_like(W)) == 0).all()
+    x, W, dy, off = _case([0, 0], 16, 24, dtype, spare=3)  # rows, but none of any expert
+    assert (moe.moe_grouped_linear(x, W, off) == 0).all()
+    assert (moe.moe_grouped_linear_wgrad(dy, x, off) == 0).all()
+    assert moe.moe_device_status() == 0
+
+
+def test_offsets_out_of_order_are_made_safe_and_reported():
+    x, W, dy, _ = _case([20, 20], 16, 24, BF16)
+    off = torch.tensor([-3, 900, 10], dtype=torch.int32, device=DEV)
+    safe = torch.tensor([0, 40, 40], dtype=torch.int32, device=DEV)
+    got = moe.moe_grouped_linear(x, W, off)
+    assert moe.moe_device_status() == -7
+    assert torch.equal(got, moe.moe_grouped_linear(x, W, safe))
+    got = moe.moe_grouped_linear_wgrad(dy, x, off)
+    assert moe.moe_device_status() == -7
+    assert torch.equal(got, moe.moe_grouped_linear_wgrad(dy, x, safe))
+    assert moe.moe_device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_gradients_by_autograd(dtype):
+    x, W, dy, off = _case([9, 0, 30], 64, 48, dtype, spare=4)
+    (_, _), (dx, dxm), (dW, dWm) = _oracle(x, W, dy, off)
+    x.requires_grad_(True)
+    W.requires_grad_(True)
+    y = moe.moe_grouped_linear(x, W, off)
+    y.backward(dy)
+    _check(x.grad, dx, dxm, 64, dtype)
+    _check(W.grad, dW, dWm, 30, dtype)
+    only, = torch.autograd.grad(moe.moe_grouped_linear(x, W, off).sum(), [W])  # expanded dy
+    ones = torch.ones_like(dy)
+    assert torch.equal(only, moe.moe_grouped_linear_wgrad(ones, x.detach(), off))
+
+
+def test_gradient_against_differences():
+    """fp32 against central differences of the fp64 formula."""
+    x, W, dy, off = _case([4, 0, 3], 8, 12, F32, seed=3)
+    o = off.tolist()
+
+    def loss(xv, Wv):
+        return sum(((xv[o[e]:o[e + 1]] @ Wv[e].t()) * dy[o[e]:o[e + 1]].double()).sum()
+                   for e in range(3))
+    x64, W64, h = x.double(), W.double(), 1e-4
+    gx = moe.moe_grouped_linear_dgrad(dy, W, off)
+    gW = moe.moe_grouped_linear_wgrad(dy, x, off)
+    for g, v, at in ((gx, x64, (2, 5)), (gx, x64, (6, 11)), (gW, W64, (0, 7, 3)), (gW, W64, (2, 0, 0))):
+        keep = v[at].item()
+        v[at] = keep + h
+        hi = loss(x64, W64)
+        v[at] = keep - h
+        lo = loss(x64, W64)
+        v[at] = keep
+        # the loss is linear in each entry: only roundings are left (sums below 100)
+        assert abs(((hi - lo) / (2 * h)).item() - g[at].item()) <= 1e-4
+
+
+def test_other_stream_and_graph():
+    x, W, dy, off = _case([50, 3, 130], 264, 136, BF16)
+    want = [moe.moe_grouped_linear(x, W, off), moe.moe_grouped_linear_dgrad(dy, W, off),
+            moe.moe_grouped_linear_wgrad(dy, x, off)]
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    y, dx, dW = (torch.empty_like(t) for t in want)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        moe.moe_grouped_linear(x, W, off, y=y)
+        moe.moe_grouped_linear_dgrad(dy, W, off, dx=dx)
+        moe.moe_grouped_linear_wgrad(dy, x, off, dW=dW)
+    for _ in range(2):
+        for t in (y, dx, dW):
+            t.fill_(float("nan"))
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip((y, dx, dW), want))
+    # new segments in the same buffers, without a new capture
+    off.copy_(torch.tensor([0, 100, 100, 183], dtype=torch.int32, device=DEV))
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(y, moe.moe_grouped_linear(x, W, off))
+    assert torch.equal(dW, moe.moe_grouped_linear_wgrad(dy, x, off))
+    assert moe.moe_device_status() == 0
+
+
+def test_refusals():
+    x, W, dy, off = _case([5, 6], 16, 24, BF16)
+    for bad in (lambda: moe.moe_grouped_linear(x[:, :16], W, off),
+                lambda: moe.moe_grouped_linear(x.t().contiguous().t(), W, off),
+                lambda: moe.moe_grouped_linear(x, W.float(), off),
+                lambda: moe.moe_grouped_linear(x, W, off.long()),
+                lambda: moe.moe_grouped_linear(x, W, off[:2]),
+                lambda: moe.moe_grouped_linear(x, W.cpu(), off),
+                lambda: moe.moe_grouped_linear(x, W, off, y=torch.empty_like(x)),
+                lambda: moe.moe_grouped_linear_dgrad(x, W, off),
+                lambda: moe.moe_grouped_linear_wgrad(dy[:5], x, off)):
+        with pytest.raises(ValueError):
+            bad()
+    with pytest.raises(moe.MoEError):  # rows of 16 bytes
+        moe.moe_grouped_linear(x[:, :20].contiguous(), W[:, :, :20].contiguous(), off)
