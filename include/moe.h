@@ -313,6 +313,54 @@ int moe_grouped_linear_wgrad(const void *dy, const void *x, const int32_t *offse
                              int M, int K, int dtype, void *dW, void *stream);
 
 /* ------------------------------------------------------------------------- *
+ * Weights in 4 bits with group scales, for decode.
+ *
+ * At decode the layer's time is the reading of the chosen experts' weights; in 4
+ * bits they are a quarter of the bytes.  (No counterpart in the pages, whose
+ * weights are bf16.)  E matrices [M, K] are held as
+ *   q       [E, M, K/2]       uint8: column 2j in the low, 2j + 1 in the high four
+ *                             bits of byte j
+ *   scales  [E, K/group, M]   bf16, group = 32, 64 or 128 columns of one row
+ * and stand for w(m, k) = (code(m, k) - 8) * scales[k / group][m].
+ * M a multiple of 8 (at most 2^20), K a multiple of group; E up to 65535.
+ *
+ * moe_quantize: scale = bf16(max |w| / 7) over the group, code = round(w / scale) + 8,
+ *   half to even, within 0..15; a group of zeros (or too small for a bf16 scale) gets
+ *   scale 0 and codes 8, a group holding a NaN or an infinity a NaN scale.
+ * moe_dequantize: the values above, each product rounded once to bf16.  For long
+ *   prompts: moe_dequantize and then moe_grouped_linear or moe_forward.
+ *
+ * moe_linear_quant: y = x w^T for tokens x [N, K] bf16, y [N, M] bf16.  The weights
+ *   are not rounded to bf16: codes times tokens are summed in fp32 per group, the
+ *   scale applied in fp32, y rounded once.  Made for N up to a few hundred; any N
+ *   works.  N = 0 is a no-op.
+ *
+ * moe_forward_quant: moe_forward (with moe_forward_clamped's limits; +infinity for
+ *   none) on bf16 tokens with every expert in 4 bits: gate_up [E, 2 d_moe, D], gate
+ *   rows first, down [E, D, d_moe], the shared expert's sh_gate_up [2 d_sh, D], gate
+ *   rows first, and sh_down [D, d_sh], all with one group size, of which D, d_moe and
+ *   d_sh are multiples.  topk_idx / topk_w, the sentinel E, ids outside [0, E] and y
+ *   as moe_forward.  The SwiGLU output is rounded to bf16, as there; the experts'
+ *   outputs are kept and summed in fp32 (slots in order, then the shared expert),
+ *   and y is rounded once.  Results are bitwise reproducible.
+ *   workspace: moe_forward_quant_workspace() bytes (0 for invalid sizes), 256-byte
+ *   aligned; not shared by calls in flight at once, captured graphs included.
+ * Errors: MOE_ERR_SHAPE, MOE_ERR_ARG, MOE_ERR_WORKSPACE.
+ */
+int moe_quantize(const void *W, int E, int M, int K, int group, void *q, void *scales, void *stream);
+int moe_dequantize(const void *q, const void *scales, int E, int M, int K, int group, void *W,
+                   void *stream);
+int moe_linear_quant(const void *x, const void *q, const void *scales, int N, int M, int K, int group,
+                     void *y, void *stream);
+size_t moe_forward_quant_workspace(int N, int D, int E, int d_moe, int d_sh, int k);
+int moe_forward_quant(const void *x, const void *gate_up, const void *gate_up_scales, const void *down,
+                      const void *down_scales, const void *sh_gate_up, const void *sh_gate_up_scales,
+                      const void *sh_down, const void *sh_down_scales, const int32_t *topk_idx,
+                      const float *topk_w, int N, int D, int E, int d_moe, int d_sh, int k, int group,
+                      float gate_max, float up_max, void *y, void *workspace, size_t ws_bytes,
+                      void *stream);
+
+/* ------------------------------------------------------------------------- *
  * Expert parallelism over peer memory.
  *
  * "GLM-5.3-Flash Module 02" (expert placement and popularity) treats the

@@ -8,7 +8,8 @@ no fallback: if libmoe.so is missing or no sm_100 GPU is current, calls raise.
     idx, w = moe_router(x, W_g, b, n_group, topk_group, k, norm_topk_prob, alpha)
     y = moe_forward(x, gate_up, down, sh_gate, sh_up, sh_down, idx, w)
 
-The experts' products by themselves, with gradients, are in products.py.
+The experts' products by themselves, with gradients, are in products.py; weights in 4 bits
+and the layer that reads them in quant.py.
 """
 
 from __future__ import annotations
@@ -29,7 +30,9 @@ __all__ = ["MoEError", "moe_router", "moe_forward", "moe_forward_workspace", "mo
            "moe_ep_forward", "moe_ep_plan_host", "moe_ep_ipc_export", "moe_ep_ipc_open",
            "moe_ep_ipc_close", "ExpertParallelGroup", "MOE_EP_COUNT", "MOE_EP_SEND",
            "MOE_EP_EXPERTS", "MOE_EP_COMBINE", "MOE_EP_ALL", "moe_bias_update",
-           "moe_grouped_linear", "moe_grouped_linear_dgrad", "moe_grouped_linear_wgrad"]
+           "moe_grouped_linear", "moe_grouped_linear_dgrad", "moe_grouped_linear_wgrad",
+           "moe_quantize", "moe_dequantize", "moe_linear_quant", "moe_forward_quant",
+           "moe_forward_quant_workspace"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libmoe.so")
@@ -49,7 +52,8 @@ EXPORTED_SYMBOLS = ("moe_router", "moe_forward_workspace", "moe_layer_forward_wo
                     "moe_debug_never_signal", "moe_profile_set_events", "moe_launch_count",
                     "moe_debug_capture_scores", "moe_debug_set_pair_mode", "moe_forward_noalloc", "moe_forward_clamped", "moe_layer_forward",
                     "moe_bias_update", "moe_grouped_linear", "moe_grouped_linear_dgrad",
-                    "moe_grouped_linear_wgrad",
+                    "moe_grouped_linear_wgrad", "moe_quantize", "moe_dequantize",
+                    "moe_linear_quant", "moe_forward_quant", "moe_forward_quant_workspace",
                     "moe_ep_symmetric_bytes",
                     "moe_ep_workspace_bytes", "moe_ep_forward", "moe_ep_plan_host",
                     "moe_ep_ipc_export", "moe_ep_ipc_open", "moe_ep_ipc_close")
@@ -118,6 +122,16 @@ def load_library():
             f.argtypes, f.restype = [P, P, P, I, I, I, I, I, P, I, P], I
         lib.moe_grouped_linear_wgrad.argtypes = [P, P, P, I, I, I, I, I, P, P]
         lib.moe_grouped_linear_wgrad.restype = I
+        for f in (lib.moe_quantize, lib.moe_dequantize):
+            f.restype = I
+        lib.moe_quantize.argtypes = [P, I, I, I, I, P, P, P]
+        lib.moe_dequantize.argtypes = [P, P, I, I, I, I, P, P]
+        lib.moe_linear_quant.argtypes = [P, P, P, I, I, I, I, P, P]
+        lib.moe_linear_quant.restype = I
+        lib.moe_forward_quant_workspace.argtypes = [I] * 6
+        lib.moe_forward_quant_workspace.restype = S
+        lib.moe_forward_quant.argtypes = [P] * 11 + [I] * 7 + [F, F, P, P, S, P]
+        lib.moe_forward_quant.restype = I
         lib.moe_ep_symmetric_bytes.argtypes = [I, I, I, I, I]
         lib.moe_ep_symmetric_bytes.restype = S
         lib.moe_ep_workspace_bytes.argtypes = [I, I, I, I, I, I, I]
@@ -488,3 +502,5 @@ class ExpertParallelGroup:
 
 from .products import (moe_grouped_linear, moe_grouped_linear_dgrad,  # noqa: E402
                        moe_grouped_linear_wgrad)
+from .quant import (moe_dequantize, moe_forward_quant, moe_forward_quant_workspace,  # noqa: E402
+                    moe_linear_quant, moe_quantize)

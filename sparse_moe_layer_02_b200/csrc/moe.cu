@@ -1449,3 +1449,4 @@ int moe_ep_ipc_close(void *dev_ptr) {
 }  // extern "C"
 
 #include "grouped_host.cuh"
+#include "quant_host.cuh"

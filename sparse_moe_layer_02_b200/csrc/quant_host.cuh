@@ -1,0 +1,346 @@
+// Host side of the 4-bit weights (moe_quantize, moe_dequantize, moe_linear_quant,
+// moe_forward_quant).  Part of moe.cu's translation unit.
+#pragma once
+
+#include "quant.cuh"
+
+namespace moe {
+namespace {
+
+bool quant_group_ok(int G) { return G == 32 || G == 64 || G == 128; }
+
+// E matrices [M, K] of codes.
+bool quant_shape_ok(int E, int M, int K, int G) {
+    return quant_group_ok(G) && E > 0 && E <= 65535 && M > 0 && M <= (1 << 20) && M % 8 == 0 && K > 0 &&
+           K <= (1 << 24) && K % G == 0;
+}
+
+// Maps of the codes and scales of E matrices [M, K] for tiles of C::R rows.
+template <typename C>
+bool make_quant_maps(CUtensorMap *mW, CUtensorMap *mS, const void *q, const void *s, int E, int M, int K,
+                     int G) {
+    auto fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t half = (cuuint64_t)K / 2, groups = (cuuint64_t)K / G;
+    cuuint32_t estr[3] = {1, 1, 1};
+    cuuint64_t wd[3] = {half, (cuuint64_t)M, (cuuint64_t)E};
+    cuuint64_t ws[2] = {half, half * M};
+    cuuint32_t wb[3] = {C::BOX, C::R / 2, 1};
+    cuuint64_t sd[3] = {(cuuint64_t)M, groups, (cuuint64_t)E};
+    cuuint64_t ss[2] = {(cuuint64_t)M * 2, (cuuint64_t)M * 2 * groups};
+    cuuint32_t sb[3] = {C::R / 2, (cuuint32_t)(C::SK / G), 1};
+    return fn(mW, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(q), wd, ws, wb, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE,
+              C::BOX == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS &&
+           fn(mS, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(s), sd, ss, sb, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int KIND, int RG, int NT>
+int launch_quant(const CUtensorMap &mW, const CUtensorMap &mS, const CUtensorMap &mW_s,
+                 const CUtensorMap &mS_s, const QuantArgs &a, size_t tiles, DeviceInfo *info,
+                 cudaStream_t st) {
+    using C = QmCfg<RG, NT>;
+    static bool attr_set[kMaxDevices] = {}; // function attributes are set per device
+    const int dev = current_device_index();
+    if (dev < 0) return MOE_ERR_CUDA;
+    {
+        std::lock_guard<std::mutex> lk(g_mu);
+        if (!attr_set[dev]) {
+            if (cudaFuncSetAttribute(quant_product_kernel<KIND, RG, NT>,
+                                     cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
+                return MOE_ERR_CUDA;
+            attr_set[dev] = true;
+        }
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)std::min<size_t>(tiles, (size_t)info->sms * 2), 1, 1);
+    cfg.blockDim = dim3(QM_THREADS, 1, 1);
+    cfg.dynamicSmemBytes = C::SMEM;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (launch_ex(cfg, quant_product_kernel<KIND, RG, NT>, mW, mS, mW_s, mS_s, a) != cudaSuccess)
+        return MOE_ERR_CUDA;
+    return launch_status();
+}
+
+template <int RG, int NT>
+int linear_quant_t(const void *q, const void *s, QuantArgs a, DeviceInfo *info, cudaStream_t st) {
+    using C = QmCfg<RG, NT>;
+    CUtensorMap mW, mS;
+    if (!make_quant_maps<C>(&mW, &mS, q, s, 1, a.ncols, a.K, a.G)) return MOE_ERR_CUDA;
+    a.nb = (a.ncols + C::R - 1) / C::R;
+    const size_t tiles = (size_t)a.nb * ((a.N + 8 * NT - 1) / (8 * NT));
+    return launch_quant<QUANT_LINEAR, RG, NT>(mW, mS, mW, mS, a, tiles, info, st);
+}
+
+// ---- the layer ----
+struct QuantWs {
+    size_t chunk_hist, counts, tile_off, meta, pos_of, perm_tok, w_perm, h, h_s, slot, osh, total;
+    int nchunks;
+    size_t rows_max;
+    int tile_rows;
+    bool direct;
+};
+
+// Tokens of a tile.  One token: every pair is its own tile, no dispatch.
+int quant_tile_tokens(int N, int k, int E) {
+    if (N <= 8) return 8;
+    return (size_t)N * k <= (size_t)8 * E ? 16 : 32;
+}
+
+bool plan_quant(int N, int D, int E, int d, int d_sh, int k, QuantWs &W) {
+    const size_t nk = (size_t)N * k;
+    if (nk > (size_t)INT32_MAX / 4) return false;
+    W.direct = N == 1;
+    W.tile_rows = quant_tile_tokens(N, k, E);
+    W.rows_max = W.direct ? nk : nk + (size_t)(W.tile_rows - 1) * std::min<size_t>(E, std::max<size_t>(nk, 1));
+    if (W.rows_max > (size_t)INT32_MAX / 4) return false;
+    W.nchunks = (int)((nk + DISPATCH_CHUNK - 1) / DISPATCH_CHUNK);
+    size_t off = 0;
+    auto take = [&](size_t bytes) {
+        const size_t at = off;
+        off = round_up(off + bytes, 256);
+        return at;
+    };
+    W.chunk_hist = take((size_t)std::max(W.nchunks, 1) * E * 4);
+    W.counts = take((size_t)E * 4);
+    W.tile_off = take((size_t)(E + 1) * 4);
+    W.meta = take(16 * 4);
+    W.pos_of = take(nk * 4);
+    W.perm_tok = take(W.rows_max * 4);
+    W.w_perm = take(W.rows_max * 4);
+    W.h = take(W.rows_max * d * 2);
+    W.h_s = take((size_t)N * d_sh * 2);
+    W.slot = take(W.rows_max * D * 4);
+    W.osh = take((size_t)N * D * 4);
+    W.total = off;
+    return true;
+}
+
+bool quant_layer_shape_ok(int N, int D, int E, int d, int d_sh, int k, int G) {
+    return N >= 0 && N <= (1 << 24) && k > 0 && k <= 32 && E <= DISPATCH_MAXE && d <= (1 << 19) &&
+           d_sh <= (1 << 19) && quant_shape_ok(E, 2 * d, D, G) && quant_shape_ok(E, D, d, G) &&
+           quant_shape_ok(1, 2 * d_sh, D, G) && quant_shape_ok(1, D, d_sh, G);
+}
+
+struct QuantLayer {
+    const void *gu, *gu_s, *dn, *dn_s, *sgu, *sgu_s, *sdn, *sdn_s;
+    int D, d, d_sh;
+};
+
+template <int RG, int NT>
+int quant_layer_t(const QuantLayer &w, QuantArgs a, const void *x, uint8_t *ws, const QuantWs &W,
+                  DeviceInfo *info, Profiler &prof, cudaStream_t st) {
+    using C = QmCfg<RG, NT>;
+    const int tt_s = (a.N + 8 * NT - 1) / (8 * NT);
+    const size_t tt_r = W.direct ? (size_t)a.k : W.rows_max / (8 * NT) + 1;
+    CUtensorMap mW, mS, mWs, mSs;
+    // gate and up rows, SwiGLU
+    if (!make_quant_maps<C>(&mW, &mS, w.gu, w.gu_s, a.E, 2 * w.d, w.D, a.G) ||
+        !make_quant_maps<C>(&mWs, &mSs, w.sgu, w.sgu_s, 1, 2 * w.d_sh, w.D, a.G))
+        return MOE_ERR_CUDA;
+    a.x = a.x_s = static_cast<const uint8_t *>(x);
+    a.row_bytes = a.row_bytes_s = w.D * 2;
+    a.K = a.K_s = w.D;
+    a.ncols = w.d;
+    a.ncols_s = w.d_sh;
+    a.nb = (w.d + C::R / 2 - 1) / (C::R / 2);
+    a.nb_s = (w.d_sh + C::R / 2 - 1) / (C::R / 2);
+    a.out = ws + W.h;
+    a.out_s = ws + W.h_s;
+    int rc = launch_quant<QUANT_GATE_UP, RG, NT>(mW, mS, mWs, mSs, a, tt_r * a.nb + (size_t)tt_s * a.nb_s,
+                                                 info, st);
+    if (rc != MOE_OK) return rc;
+    prof.mark();
+    // down
+    if (!make_quant_maps<C>(&mW, &mS, w.dn, w.dn_s, a.E, w.D, w.d, a.G) ||
+        !make_quant_maps<C>(&mWs, &mSs, w.sdn, w.sdn_s, 1, w.D, w.d_sh, a.G))
+        return MOE_ERR_CUDA;
+    a.x = ws + W.h;
+    a.x_s = ws + W.h_s;
+    a.row_bytes = w.d * 2;
+    a.row_bytes_s = w.d_sh * 2;
+    a.K = w.d;
+    a.K_s = w.d_sh;
+    a.ncols = a.ncols_s = w.D;
+    a.nb = a.nb_s = (w.D + C::R - 1) / C::R;
+    a.out = ws + W.slot;
+    a.out_s = ws + W.osh;
+    rc = launch_quant<QUANT_DOWN, RG, NT>(mW, mS, mWs, mSs, a, tt_r * a.nb + (size_t)tt_s * a.nb_s, info, st);
+    if (rc == MOE_OK) prof.mark();
+    return rc;
+}
+
+}  // namespace
+}  // namespace moe
+
+extern "C" {
+
+int moe_quantize(const void *W, int E, int M, int K, int group, void *q, void *scales, void *stream) {
+    if (!quant_shape_ok(E, M, K, group)) return MOE_ERR_SHAPE;
+    for (const void *p : {W, (const void *)q, (const void *)scales})
+        if (!p || !aligned16(p)) return MOE_ERR_ARG;
+    DeviceInfo *dev = nullptr;
+    int rc = current_device_info(&dev);
+    if (rc != MOE_OK) return rc;
+    if (dev->major != 10) return MOE_ERR_NO_DEVICE;
+    const dim3 grid((K + QZ_COLS - 1) / QZ_COLS, (M + QZ_ROWS - 1) / QZ_ROWS, E);
+    quantize_kernel<<<grid, QZ_THREADS, 0, static_cast<cudaStream_t>(stream)>>>(
+        static_cast<const __nv_bfloat16 *>(W), static_cast<uint8_t *>(q), static_cast<__nv_bfloat16 *>(scales),
+        M, K, group);
+    return launch_status();
+}
+
+int moe_dequantize(const void *q, const void *scales, int E, int M, int K, int group, void *W, void *stream) {
+    if (!quant_shape_ok(E, M, K, group)) return MOE_ERR_SHAPE;
+    for (const void *p : {q, scales, (const void *)W})
+        if (!p || !aligned16(p)) return MOE_ERR_ARG;
+    DeviceInfo *dev = nullptr;
+    int rc = current_device_info(&dev);
+    if (rc != MOE_OK) return rc;
+    if (dev->major != 10) return MOE_ERR_NO_DEVICE;
+    const dim3 grid((K + QZ_COLS - 1) / QZ_COLS, (M + QZ_ROWS - 1) / QZ_ROWS, E);
+    dequantize_kernel<<<grid, QZ_THREADS, 0, static_cast<cudaStream_t>(stream)>>>(
+        static_cast<const uint8_t *>(q), static_cast<const __nv_bfloat16 *>(scales),
+        static_cast<__nv_bfloat16 *>(W), M, K, group);
+    return launch_status();
+}
+
+int moe_linear_quant(const void *x, const void *q, const void *scales, int N, int M, int K, int group,
+                     void *y, void *stream) {
+    if (N < 0 || N > (1 << 24) || !quant_shape_ok(1, M, K, group)) return MOE_ERR_SHAPE;
+    if (((size_t)M / 32 + 1) * ((size_t)N / 8 + 1) > (size_t)INT32_MAX / 2) return MOE_ERR_SHAPE;
+    if (N == 0) return MOE_OK;
+    for (const void *p : {x, q, scales, (const void *)y})
+        if (!p || !aligned16(p)) return MOE_ERR_ARG;
+    DeviceInfo *dev = nullptr;
+    int rc = current_device_info(&dev);
+    if (rc != MOE_OK) return rc;
+    if (dev->major != 10) return MOE_ERR_NO_DEVICE;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    QuantArgs a = {};
+    a.x = static_cast<const uint8_t *>(x);
+    a.row_bytes = K * 2;
+    a.N = N;
+    a.G = group;
+    a.K = K;
+    a.ncols = M;
+    a.out = y;
+    a.wait_limit_ns = g_wait_limit_ns;
+    if (N <= 8) {
+        // Few rows: 32-row tiles, so that more SMs have one.
+        if ((size_t)M < (size_t)64 * 2 * dev->sms) return linear_quant_t<1, 1>(q, scales, a, dev, st);
+        return linear_quant_t<2, 1>(q, scales, a, dev, st);
+    }
+    if (N <= 16) return linear_quant_t<2, 2>(q, scales, a, dev, st);
+    return linear_quant_t<4, 4>(q, scales, a, dev, st);
+}
+
+size_t moe_forward_quant_workspace(int N, int D, int E, int d_moe, int d_sh, int k) {
+    if (N < 0 || D <= 0 || E <= 0 || E > DISPATCH_MAXE || d_moe <= 0 || d_sh <= 0 || k <= 0 || k > 32) return 0;
+    QuantWs W;
+    return plan_quant(N, D, E, d_moe, d_sh, k, W) ? W.total : 0;
+}
+
+int moe_forward_quant(const void *x, const void *gate_up, const void *gate_up_scales, const void *down,
+                      const void *down_scales, const void *sh_gate_up, const void *sh_gate_up_scales,
+                      const void *sh_down, const void *sh_down_scales, const int32_t *topk_idx,
+                      const float *topk_w, int N, int D, int E, int d_moe, int d_sh, int k, int group,
+                      float gate_max, float up_max, void *y, void *workspace, size_t ws_bytes,
+                      void *stream) {
+    if (gate_max != gate_max || up_max != up_max || up_max < 0.f) return MOE_ERR_ARG;
+    QuantWs W;
+    if (!quant_layer_shape_ok(N, D, E, d_moe, d_sh, k, group) || !plan_quant(N, D, E, d_moe, d_sh, k, W))
+        return MOE_ERR_SHAPE;
+    if ((W.rows_max / 8 + 1) * ((size_t)std::max(D, std::max(d_moe, d_sh)) / 32 + 1) +
+            ((size_t)N / 8 + 1) * ((size_t)std::max(D, d_sh) / 16 + 1) > (size_t)INT32_MAX / 2)
+        return MOE_ERR_SHAPE; // tile numbers are 32-bit
+    if (N == 0) return MOE_OK;
+    for (const void *p : {x, gate_up, gate_up_scales, down, down_scales, sh_gate_up, sh_gate_up_scales,
+                          sh_down, sh_down_scales, (const void *)topk_idx, (const void *)topk_w,
+                          (const void *)y})
+        if (!p || !aligned16(p)) return MOE_ERR_ARG;
+    if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) || ws_bytes < W.total)
+        return MOE_ERR_WORKSPACE;
+    DeviceInfo *dev = nullptr;
+    int rc = current_device_info(&dev);
+    if (rc != MOE_OK) return rc;
+    if (dev->major != 10) return MOE_ERR_NO_DEVICE;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    Profiler prof(st);
+
+    QuantArgs a = {};
+    a.N = N;
+    a.E = E;
+    a.k = k;
+    a.G = group;
+    a.direct = W.direct ? 1 : 0;
+    a.topk_idx = topk_idx;
+    a.topk_w = topk_w;
+    a.gate_max = gate_max;
+    a.up_max = up_max;
+    a.wait_limit_ns = g_wait_limit_ns;
+    DispatchParams dp = {};
+    if (!W.direct) {
+        dp.topk_idx = topk_idx;
+        dp.topk_w = topk_w;
+        dp.N = N;
+        dp.k = k;
+        dp.E = E;
+        dp.nchunks = W.nchunks;
+        dp.tile_rows = W.tile_rows;
+        dp.chunk_hist = reinterpret_cast<int32_t *>(ws + W.chunk_hist);
+        dp.counts = reinterpret_cast<int32_t *>(ws + W.counts);
+        dp.tile_off = reinterpret_cast<int32_t *>(ws + W.tile_off);
+        dp.meta = reinterpret_cast<int32_t *>(ws + W.meta);
+        dp.pos_of = reinterpret_cast<int32_t *>(ws + W.pos_of);
+        dp.perm_tok = reinterpret_cast<int32_t *>(ws + W.perm_tok);
+        dp.w_perm = reinterpret_cast<float *>(ws + W.w_perm);
+        if ((size_t)N * k <= DISPATCH_SMALL_IDS) {
+            dispatch_small_kernel<<<1, DISPATCH_SMALL_THREADS, 0, st>>>(dp);
+            if ((rc = launched(prof)) != MOE_OK) return rc;
+        } else {
+            dispatch_count_kernel<<<W.nchunks, DISPATCH_THREADS, 0, st>>>(dp);
+            if ((rc = launch_status()) != MOE_OK) return rc;
+            dispatch_scan_kernel<<<1, DISPATCH_MAXE, 0, st>>>(dp);
+            if ((rc = launch_status()) != MOE_OK) return rc;
+            dispatch_scatter_kernel<<<W.nchunks, DISPATCH_THREADS, 0, st>>>(dp);
+            if ((rc = launched(prof)) != MOE_OK) return rc;
+        }
+        a.tile_off = dp.tile_off;
+        a.counts = dp.counts;
+        a.perm_tok = dp.perm_tok;
+        a.w_perm = dp.w_perm;
+    } else {
+        prof.mark();
+    }
+    const QuantLayer w = {gate_up, gate_up_scales, down, down_scales, sh_gate_up, sh_gate_up_scales,
+                          sh_down, sh_down_scales, D, d_moe, d_sh};
+    rc = W.tile_rows == 8    ? quant_layer_t<2, 1>(w, a, x, ws, W, dev, prof, st)
+         : W.tile_rows == 16 ? quant_layer_t<2, 2>(w, a, x, ws, W, dev, prof, st)
+                             : quant_layer_t<4, 4>(w, a, x, ws, W, dev, prof, st);
+    if (rc != MOE_OK) return rc;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(N, (D + 1023) / 1024, 1);
+    cfg.blockDim = dim3(128, 1, 1);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (launch_ex(cfg, quant_combine_kernel, a, (const float *)(ws + W.slot), (const float *)(ws + W.osh),
+                  (const int32_t *)dp.pos_of, static_cast<__nv_bfloat16 *>(y), D) != cudaSuccess)
+        return MOE_ERR_CUDA;
+    return launched(prof);
+}
+
+}  // extern "C"

@@ -1,0 +1,131 @@
+"""Weights in 4 bits with group scales, and the products that read them.
+
+    q, scales = moe_quantize(W, group)             # W [..., M, K] bf16
+    W = moe_dequantize(q, scales)
+    y = moe_linear_quant(x, q, scales)             # x [N, K] bf16, q [M, K/2]
+    y = moe_forward_quant(x, gate_up, down, sh_gate_up, sh_down, topk_idx, topk_w)
+
+A matrix [M, K] is a pair (q, scales): q uint8 [M, K/2], column 2j in the low and 2j + 1 in
+the high four bits of byte j, scales bf16 [K/group, M]; its value at (m, k) is
+(code - 8) * scales[k // group, m].  The group size is read off the shapes.
+Every call runs on the tensors' own device, on that device's current stream unless a
+stream is given, and needs all tensors there.
+"""
+
+from __future__ import annotations
+
+import torch
+
+from . import _check, _dev, load_library
+from .products import _device, _on, _out, _stream_on
+
+__all__ = ["moe_quantize", "moe_dequantize", "moe_linear_quant", "moe_forward_quant",
+           "moe_forward_quant_workspace"]
+
+
+def _pair(q, scales, lead, name):
+    """(M, K, group) of 4-bit weights with `lead` leading dimensions."""
+    if q.dtype != torch.uint8 or scales.dtype != torch.bfloat16:
+        raise ValueError("%s must be (uint8 codes, bfloat16 scales)" % name)
+    if q.dim() != lead + 2 or scales.dim() != lead + 2 or q.shape[:lead] != scales.shape[:lead]:
+        raise ValueError("%s: codes [.., M, K/2] and scales [.., K/group, M] do not agree" % name)
+    M, K, groups = q.shape[-2], 2 * q.shape[-1], scales.shape[-2]
+    if scales.shape[-1] != M or groups == 0 or K % groups:
+        raise ValueError("%s: codes [.., M, K/2] and scales [.., K/group, M] do not agree" % name)
+    return M, K, K // groups
+
+
+def moe_quantize(W, group: int = 128, q=None, scales=None, stream=None):
+    """(q, scales) of bf16 weights W [..., M, K], group = 32, 64 or 128."""
+    if W.dim() < 2 or W.dtype != torch.bfloat16:
+        raise ValueError("W must be bfloat16 [..., M, K]")
+    dev = _device(W)
+    lead, (M, K) = tuple(W.shape[:-2]), W.shape[-2:]
+    if group not in (32, 64, 128) or K % group:
+        raise ValueError("group must be 32, 64 or 128 and divide K")
+    q = _out(q, lead + (M, K // 2), torch.uint8, dev, "q")
+    scales = _out(scales, lead + (K // group, M), torch.bfloat16, dev, "scales")
+    E = W.numel() // (M * K) if M * K else 0
+    with _on(dev):
+        _check(load_library().moe_quantize(_dev(W, "W"), E, M, K, group, _dev(q, "q"),
+                                           _dev(scales, "scales"), _stream_on(dev, stream)),
+               "moe_quantize")
+    return q, scales
+
+
+def moe_dequantize(q, scales, W=None, stream=None):
+    """The bf16 values [..., M, K] of 4-bit weights."""
+    M, K, group = _pair(q, scales, q.dim() - 2, "the weights")
+    dev = _device(q, scales)
+    W = _out(W, tuple(q.shape[:-2]) + (M, K), torch.bfloat16, dev, "W")
+    E = W.numel() // (M * K) if M * K else 0
+    with _on(dev):
+        _check(load_library().moe_dequantize(_dev(q, "q"), _dev(scales, "scales"), E, M, K, group,
+                                             _dev(W, "W"), _stream_on(dev, stream)),
+               "moe_dequantize")
+    return W
+
+
+def moe_linear_quant(x, q, scales, y=None, stream=None):
+    """y [N, M] = x W^T for tokens x [N, K] bf16 and one matrix in 4 bits."""
+    M, K, group = _pair(q, scales, 0, "the weights")
+    if x.dim() != 2 or x.shape[1] != K or x.dtype != torch.bfloat16:
+        raise ValueError("x must be bfloat16 [N, K]")
+    dev = _device(x, q, scales)
+    N = x.shape[0]
+    y = _out(y, (N, M), torch.bfloat16, dev, "y")
+    with _on(dev):
+        _check(load_library().moe_linear_quant(_dev(x, "x"), _dev(q, "q"), _dev(scales, "scales"),
+                                               N, M, K, group, _dev(y, "y"),
+                                               _stream_on(dev, stream)), "moe_linear_quant")
+    return y
+
+
+def moe_forward_quant_workspace(N: int, D: int, E: int, d_moe: int, d_sh: int, k: int) -> int:
+    """Bytes of device workspace moe_forward_quant needs (0 for invalid sizes)."""
+    return int(load_library().moe_forward_quant_workspace(N, D, E, d_moe, d_sh, k))
+
+
+def moe_forward_quant(x, gate_up, down, sh_gate_up, sh_down, topk_idx, topk_w, y=None,
+                      workspace=None, stream=None, gate_max=None, up_max=None):
+    """moe_forward with all experts in 4 bits; returns y [N, D] bf16.
+
+    gate_up, down, sh_gate_up, sh_down: (q, scales) pairs of [E, 2 d_moe, D] (gate rows
+    first), [E, D, d_moe], [2 d_sh, D] (gate rows first) and [D, d_sh], one group size.
+    topk_idx [N, k] int32 (id E: no expert), topk_w [N, k] fp32.  gate_max / up_max: the
+    clamped SwiGLU's limits."""
+    two_d, D, group = _pair(*gate_up, 1, "gate_up")
+    D2, d, g2 = _pair(*down, 1, "down")
+    two_ds, D3, g3 = _pair(*sh_gate_up, 0, "sh_gate_up")
+    D4, d_sh, g4 = _pair(*sh_down, 0, "sh_down")
+    E = gate_up[0].shape[0]
+    if x.dim() != 2 or x.shape[1] != D or x.dtype != torch.bfloat16:
+        raise ValueError("x must be bfloat16 [N, D]")
+    if (D2, D3, D4) != (D, D, D) or two_d != 2 * d or two_ds != 2 * d_sh \
+            or down[0].shape[0] != E or (g2, g3, g4) != (group,) * 3:
+        raise ValueError("inconsistent expert shapes or group sizes")
+    N = x.shape[0]
+    if topk_idx.dim() != 2 or topk_idx.shape[0] != N or topk_w.shape != topk_idx.shape \
+            or topk_idx.dtype != torch.int32 or topk_w.dtype != torch.float32:
+        raise ValueError("topk_idx must be int32 and topk_w float32, both [N, k]")
+    k = topk_idx.shape[1]
+    dev = _device(x, *gate_up, *down, *sh_gate_up, *sh_down, topk_idx, topk_w)
+    y = _out(y, (N, D), torch.bfloat16, dev, "y")
+    if workspace is None:
+        workspace = torch.empty(max(moe_forward_quant_workspace(N, D, E, d, d_sh, k), 256),
+                                dtype=torch.uint8, device=x.device)
+    elif workspace.device != x.device:
+        raise ValueError("the workspace must be on the inputs' device")
+    inf = float("inf")
+    with _on(dev):
+        _check(load_library().moe_forward_quant(
+            _dev(x, "x"), _dev(gate_up[0], "gate_up"), _dev(gate_up[1], "gate_up scales"),
+            _dev(down[0], "down"), _dev(down[1], "down scales"),
+            _dev(sh_gate_up[0], "sh_gate_up"), _dev(sh_gate_up[1], "sh_gate_up scales"),
+            _dev(sh_down[0], "sh_down"), _dev(sh_down[1], "sh_down scales"),
+            _dev(topk_idx, "topk_idx"), _dev(topk_w, "topk_w"), N, D, E, d, d_sh, k, group,
+            inf if gate_max is None else float(gate_max), inf if up_max is None else float(up_max),
+            _dev(y, "y"), _dev(workspace, "workspace"),
+            workspace.numel() * workspace.element_size(), _stream_on(dev, stream)),
+            "moe_forward_quant")
+    return y

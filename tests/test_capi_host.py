@@ -161,3 +161,47 @@ def test_grouped_products_reject_bad_arguments():
     assert call(lib.moe_grouped_linear, rows=0, a=None, out=None) == 0
     assert call(lib.moe_grouped_linear_dgrad, rows=0, a=None, out=None) == 0
     assert call(lib.moe_grouped_linear_wgrad, rows=0, a=None, b=None, out=None) == -1
+
+
+def test_quantized_weights_reject_bad_arguments():
+    lib = moe.load_library()
+    for f in (lib.moe_quantize, lib.moe_dequantize):
+        call = lambda E=2, M=16, K=256, G=128, p=(16, 16, 16), f=f: (
+            f(p[0], E, M, K, G, p[1], p[2], None) if f is lib.moe_quantize
+            else f(p[0], p[1], E, M, K, G, p[2], None))
+        assert call(G=48) == -2 and call(G=0) == -2 and call(K=192) == -2 and call(M=12) == -2
+        assert call(E=0) == -2 and call(E=65536) == -2 and call(M=0) == -2 and call(K=0) == -2
+        for bad in (None, 8):
+            for i in range(3):
+                p = [16, 16, 16]
+                p[i] = bad
+                assert call(p=p) == -1
+    call = lambda N=4, M=16, K=256, G=64, p=(16, 16, 16, 16): lib.moe_linear_quant(
+        p[0], p[1], p[2], N, M, K, G, p[3], None)
+    assert call(G=16) == -2 and call(K=224) == -2 and call(M=4) == -2 and call(N=-1) == -2
+    assert call(N=1 << 24, M=1 << 20) == -2                    # tile numbers are 32-bit
+    assert call(p=(None, 16, 16, 16)) == -1 and call(p=(16, 16, 24, 16)) == -1
+    assert call(N=0, p=(None,) * 4) == 0
+
+
+def test_quantized_layer_rejects_bad_arguments():
+    lib = moe.load_library()
+
+    def call(N=4, D=256, E=8, d=128, d_sh=128, k=2, G=64, gm=1.0, um=1.0, ptr=None, bad=None,
+             ws=256, wsb=1 << 40):
+        p = [16] * 12
+        if ptr is not None:
+            p[ptr] = bad
+        return lib.moe_forward_quant(*p[:11], N, D, E, d, d_sh, k, G, gm, um, p[11], ws, wsb, None)
+    nan = float("nan")
+    assert call(gm=nan) == -1 and call(um=nan) == -1 and call(um=-1.0) == -1
+    assert call(G=96) == -2 and call(D=288) == -2 and call(d=96) == -2 and call(d_sh=32) == -2
+    assert call(E=0) == -2 and call(E=513) == -2 and call(k=0) == -2 and call(k=33) == -2
+    assert call(N=-1) == -2
+    for i in range(12):
+        assert call(ptr=i) == -1 and call(ptr=i, bad=20) == -1
+    assert call(ws=None) == -4 and call(ws=16) == -4 and call(wsb=1000) == -4
+    assert call(N=0, ws=None) == 0
+    w = lib.moe_forward_quant_workspace
+    assert 0 < w(1, 256, 8, 128, 128, 2) < w(64, 256, 8, 128, 128, 2)
+    assert w(4, 256, 8, 128, 128, 0) == 0 and w(4, 256, 513, 128, 128, 2) == 0
