@@ -16,57 +16,76 @@
 namespace moe {
 
 // ---------------------------------------------------------------------------
-// Conversion.  s = bf16(max|w| / 7) over the group, q = round(w / s) + 8 (half to
-// even; -8..7).  One block takes 32 rows x 256 columns; a warp takes 4 rows, a lane 8
-// columns of each, so a group is 4, 8 or 16 neighbouring lanes and its maximum two to
-// four shuffles.  The block's scales pass through shared memory to be stored 64 bytes
-// at a time.  Bound by memory: 2.5 bytes + 2/G per weight either way.
+// Conversion.  s = bf16(max|w| / 7) over the group, code = round(w / s) + 8 (half to
+// even).  A warp takes rows of 256 columns, a lane 8 columns of each, so a group is 4, 8
+// or 16 neighbouring lanes and its maximum two to four shuffles.  A block's scales pass
+// through shared memory to be stored a row of them at a time.  Bound by memory: 2.5
+// bytes + 2/G per weight either way; a warp keeps 4 rows (64 bytes a lane) in flight to
+// quantize and 8 rows (32 bytes a lane) to dequantize.
+//
+// w / s is taken as w * (1/s), rounded to a multiple of 2^-12 on the way (one
+// multiply-add with 1.5 * 2^11).  That gives round(w / s) exactly: w and s have 8-bit
+// significands, so a quotient between 1/4 and 8 either is a multiple of 1/2 or lies at
+// least 2^-11 away from every odd multiple of 1/2, while the product is within 2^-19 of
+// the quotient.  |w / s| < 7.5 for scales that are normal numbers; below 2^-120, where s
+// or 1/s is not, the code comes from the division and is clamped.
 // ---------------------------------------------------------------------------
-constexpr int QZ_ROWS = 32, QZ_COLS = 256, QZ_THREADS = 256;
+constexpr int QZ_ROWS = 32, DQ_ROWS = 64, QZ_COLS = 256, QZ_THREADS = 256;
 
 __global__ void __launch_bounds__(QZ_THREADS) quantize_kernel(const __nv_bfloat16 *__restrict__ W,
                                                               uint8_t *__restrict__ q,
                                                               __nv_bfloat16 *__restrict__ s, int M, int K,
                                                               int G) {
+    constexpr int RW = QZ_ROWS / 8; // rows of a warp
     __shared__ __nv_bfloat16 ss[QZ_COLS / 32][QZ_ROWS];
     const int lane = lane_id(), warp = warp_id();
     const int k = blockIdx.x * QZ_COLS + lane * 8, m0 = blockIdx.y * QZ_ROWS;
     const size_t e = blockIdx.z;
     const int per = G >> 3; // lanes of a group
-    uint4 v[4];
+    uint4 v[RW];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int m = m0 + warp * 4 + i;
+    for (int i = 0; i < RW; ++i) {
+        const int m = m0 + warp * RW + i;
         v[i] = make_uint4(0u, 0u, 0u, 0u);
         if (m < M && k < K)
             v[i] = __ldcs(reinterpret_cast<const uint4 *>(W + (e * M + m) * (size_t)K + k));
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int m = m0 + warp * 4 + i;
+    for (int i = 0; i < RW; ++i) {
+        const int m = m0 + warp * RW + i;
+        // The largest magnitude, two columns at a time (a NaN wins over all).
+        const __nv_bfloat162 *b = reinterpret_cast<const __nv_bfloat162 *>(&v[i]);
+        __nv_bfloat162 t2 = __hmax2_nan(__hmax2_nan(__habs2(b[0]), __habs2(b[1])),
+                                        __hmax2_nan(__habs2(b[2]), __habs2(b[3])));
+        for (int d = 1; d < per; d <<= 1) t2 = __hmax2_nan(t2, __shfl_xor_sync(0xffffffffu, t2, d));
+        const float top = __bfloat162float(__hmax_nan(__low2bfloat16(t2), __high2bfloat16(t2)));
+        __nv_bfloat16 sb = __float2bfloat16_rn(top / 7.0f);
+        if (!(top < INFINITY)) sb = __ushort_as_bfloat16(0x7FFF); // every value NaN
+        const float sf = __bfloat162float(sb);
         float w[8];
         unpack_bf16x2(v[i].x, w[0], w[1]);
         unpack_bf16x2(v[i].y, w[2], w[3]);
         unpack_bf16x2(v[i].z, w[4], w[5]);
         unpack_bf16x2(v[i].w, w[6], w[7]);
-        // The maximum of the magnitudes' bit patterns: a NaN is above infinity, so
-        // neither is lost.
-        uint32_t top = 0;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(w[j]) & 0x7FFFFFFFu);
-        for (int d = 1; d < per; d <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
-        __nv_bfloat16 sb = __float2bfloat16_rn(__uint_as_float(top) / 7.0f);
-        if (top >= 0x7F800000u) sb = __ushort_as_bfloat16(0x7FFF); // not finite: every value NaN
-        const float sf = __bfloat162float(sb);
         uint32_t c = 0;
+        if (sf >= 0x1p-120f) {
+            const float r = 1.0f / sf;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            // s = 0 (all zero, or too small for bf16) and s = NaN take the code of 0
-            const float t = sf > 0.f ? fminf(fmaxf(rintf(w[j] / sf), -8.f), 7.f) : 0.f;
-            c |= (uint32_t)((int)t + 8) << (4 * j);
+            for (int j = 0; j < 8; ++j) {
+                const float t = fmaf(w[j], r, 3072.0f) - 3072.0f;    // a multiple of 2^-12
+                const uint32_t n = __float_as_uint(t + 12582920.0f); // 1.5 * 2^23 + 8: code in the low bits
+                c |= (n & 15u) << (4 * j);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                // s = 0 (all zero, or too small for bf16) and s = NaN take the code of 0
+                const float t = sf > 0.f ? fminf(fmaxf(rintf(w[j] / sf), -8.f), 7.f) : 0.f;
+                c |= (uint32_t)((int)t + 8) << (4 * j);
+            }
         }
         if (m < M && k < K) *reinterpret_cast<uint32_t *>(q + (e * M + m) * (size_t)(K / 2) + k / 2) = c;
-        if ((lane & (per - 1)) == 0) ss[lane / per][warp * 4 + i] = sb;
+        if ((lane & (per - 1)) == 0) ss[lane / per][warp * RW + i] = sb;
     }
     __syncthreads();
     const int groups = QZ_COLS / G;
@@ -79,34 +98,36 @@ __global__ void __launch_bounds__(QZ_THREADS) dequantize_kernel(const uint8_t *_
                                                                 const __nv_bfloat16 *__restrict__ s,
                                                                 __nv_bfloat16 *__restrict__ W, int M, int K,
                                                                 int G) {
-    __shared__ __nv_bfloat16 ss[QZ_COLS / 32][QZ_ROWS];
+    constexpr int RW = DQ_ROWS / 8;
+    __shared__ __nv_bfloat16 ss[QZ_COLS / 32][DQ_ROWS];
     const int lane = lane_id(), warp = warp_id();
-    const int k = blockIdx.x * QZ_COLS + lane * 8, m0 = blockIdx.y * QZ_ROWS;
+    const int k = blockIdx.x * QZ_COLS + lane * 8, m0 = blockIdx.y * DQ_ROWS;
     const size_t e = blockIdx.z;
-    uint32_t c[4];
+    uint32_t c[RW];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int m = m0 + warp * 4 + i;
+    for (int i = 0; i < RW; ++i) {
+        const int m = m0 + warp * RW + i;
         c[i] = 0;
         if (m < M && k < K)
             c[i] = __ldcs(reinterpret_cast<const uint32_t *>(q + (e * M + m) * (size_t)(K / 2) + k / 2));
     }
     const int groups = QZ_COLS / G;
-    const int g = threadIdx.x / QZ_ROWS, r = threadIdx.x % QZ_ROWS;
-    const int kg = blockIdx.x * groups + g;
-    if (g < groups && kg < K / G && m0 + r < M) ss[g][r] = s[(e * (K / G) + kg) * (size_t)M + m0 + r];
+    for (int j = threadIdx.x; j < groups * DQ_ROWS; j += QZ_THREADS) {
+        const int g = j / DQ_ROWS, r = j % DQ_ROWS, kg = blockIdx.x * groups + g;
+        if (kg < K / G && m0 + r < M) ss[g][r] = s[(e * (K / G) + kg) * (size_t)M + m0 + r];
+    }
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int m = m0 + warp * 4 + i;
+    for (int i = 0; i < RW; ++i) {
+        const int m = m0 + warp * RW + i;
         if (m >= M || k >= K) continue;
-        const float sf = __bfloat162float(ss[lane * 8 / G][warp * 4 + i]);
+        const float sf = __bfloat162float(ss[lane * 8 / G][warp * RW + i]);
         uint32_t o[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) // products of 4 and 8 bits are exact in fp32
             o[j] = pack_bf16x2((float)((int)((c[i] >> (8 * j)) & 15u) - 8) * sf,
                                (float)((int)((c[i] >> (8 * j + 4)) & 15u) - 8) * sf);
-        *reinterpret_cast<uint4 *>(W + (e * M + m) * (size_t)K + k) = make_uint4(o[0], o[1], o[2], o[3]);
+        __stcs(reinterpret_cast<uint4 *>(W + (e * M + m) * (size_t)K + k), make_uint4(o[0], o[1], o[2], o[3]));
     }
 }
 
@@ -119,44 +140,63 @@ __global__ void __launch_bounds__(QZ_THREADS) dequantize_kernel(const uint8_t *_
 //   The sum over k does not care about order, only that both operands use the same.
 //   A thread's word holds columns k0..k7; (word >> 4i) & 0x000F000F puts columns i and
 //   i+4 into the halves of a register, so the MMA's pairs are (0,4), (1,5), (2,6),
-//   (3,7), and the tokens' registers are paired alike by four byte permutes.
-// - A code c becomes bf16 by setting the exponent of 128 above it (128 + c, exact in 8
-//   bits) and subtracting 136.  The group's sum of integers times tokens is fp32 in
-//   the MMA; its scale is applied once per group, in fp32.
+//   (3,7), and the tokens are brought into the same order.
+// - A code is a bf16 as it stands: with exponent bits 0 the bits 0-7 of a bf16 are an
+//   integer times 2^-133 (the lowest normal exponent continues the subnormals), so a
+//   masked code at bits 0-3 is c 2^-133 and one at bits 4-7 is 16 c 2^-133, exactly.
+//   Five logic operations unpack eight codes.  The tokens are scaled by 2^64, or 2^60
+//   against the factor 16, so products lie around 2^-69, far inside fp32; tokens of
+//   2^63 and more become infinite.
+// - The code's offset of 8 is the same for every row: -8 times the group's sum of the
+//   token, which is formed once per stage.
+// - A group's sum is fp32 in the MMA; its scale, with 2^69 on it, is applied once per
+//   group in fp32 (scales of 2^58 and more become infinite).
 //
 // tcgen05 would want the bf16 weights in shared memory first (four times the codes'
 // bytes written and read again) and has nothing to gain: the tensor work is small here.
 //
-// A block is one producer warp and eight consumer warps: RG groups of 32 rows x KS
-// slices of 64 columns (RG * KS = 8).  The producer fills a ring: codes and scales by
-// TMA, the tokens' rows by 16-byte asynchronous copies, which may come from anywhere
-// (a routed token's row is fetched where it lies, without a gather pass) and are zero
-// for absent tokens and columns past K.  At the end of a tile the KS partial sums are
-// added in order through shared memory.  Two blocks share an SM.
+// A block is one producer warp, one shaper warp and eight consumer warps: RG groups of 16 MT
+// rows x KS slices of KW columns (RG * KS = 8).  The producer fills a ring: codes and
+// scales by TMA, each token's columns by a bulk copy, which may come from anywhere (a
+// routed token's row is fetched where it lies, without a gather pass).  A group's rows are 8 MT of the tile's
+// first half and as many of its second, so a gate and its up value meet in one thread.  KS = 1 keeps
+// a row's whole sum in one warp: no exchange, no barrier among the consumers; KS > 1, for
+// few tiles, adds the slices' sums in order through shared memory.  With fewer tiles
+// than SMs (or hardly more) the blocks of a cluster also share a tile's columns, and
+// exchange their sums through distributed shared memory.
 // ---------------------------------------------------------------------------
 enum QuantKind { QUANT_LINEAR = 0, QUANT_GATE_UP = 1, QUANT_DOWN = 2 };
 
-constexpr int QM_THREADS = 288;
+constexpr int QM_THREADS = 320;
 constexpr int QM_CONSUMERS = 256;
 constexpr int QM_MAXE = 512;
 
-template <int RG, int NT> struct QmCfg {
+constexpr int qm_max(int a, int b) { return a > b ? a : b; }
+template <int RG, int MT, int KW, int NT, int G> struct QmCfg {
     static constexpr int KS = 8 / RG;
-    static constexpr int R = 32 * RG;            // weight rows of a tile
-    static constexpr int SK = 64 * KS;           // columns of a stage
+    static constexpr int R = 16 * MT * RG, HALF = R / 2; // weight rows of a tile
+    static constexpr int SK = KW * KS;              // columns of a stage
+    static constexpr int UNIT = G < KW ? G : KW;    // columns of a slice under one scale
+    static constexpr int BLOCKS = NT <= 2 ? 2 : 1; // per SM
     static constexpr int BOX = SK / 2 < 128 ? SK / 2 : 128; // bytes of a code box's row = swizzle span
     static constexpr int NBOX = SK / 2 / BOX;
-    static constexpr int W_BYTES = R * SK / 2;   // 8 KiB
-    static constexpr int S_BYTES = R * (SK / 32) * 2; // 1 KiB (G = 32; fewer for larger G)
-    static constexpr int X_BYTES = NT * 8 * SK * 2;
-    static constexpr int STAGE = W_BYTES + S_BYTES + X_BYTES;
-    static constexpr int LD = R + 4;             // floats per token in the sums' buffer
-    static constexpr int RED_BYTES = KS * 8 * NT * LD * 4;
-    static constexpr int TAB_BYTES = 256 + (2 * QM_MAXE + 2) * 4;
-    // two blocks per SM
-    static constexpr int STAGES = (113 * 1024 - 1024 - RED_BYTES - TAB_BYTES) / STAGE;
-    static constexpr int SMEM = 1024 + STAGES * STAGE + RED_BYTES + TAB_BYTES;
-    static_assert(STAGES >= 2 && STAGES <= 15, "ring depth");
+    static constexpr int W_BYTES = R * SK / 2;
+    static constexpr int S_HALF = qm_max(128, HALF * (SK / G) * 2);
+    static constexpr int XLD = SK * 2 + 64;         // a token's bytes: an odd multiple of 64
+    static constexpr int X_BYTES = NT * 8 * XLD;
+    static constexpr int PIECES = SK / 8;               // 16-byte pieces of a token's stage
+    static constexpr int TURNS = NT * 8 * PIECES / 32;  // of a warp over all tokens
+    static constexpr int U_BYTES = SK / UNIT * 8 * NT * 4; // the tokens' sums
+    static constexpr int STAGE = W_BYTES + 2 * S_HALF + X_BYTES + U_BYTES;
+    static constexpr int LD = R + 4; // floats per token in the sums' buffer
+    static constexpr int RED_BYTES = KS > 1 ? KS * 8 * NT * LD * 4 : 0;
+    static constexpr int JOIN_BYTES = KS > 1 ? 8 * NT * R * 4 : 0; // sums from the blocks of a cluster
+    static constexpr int TAB_BYTES = 384 + (2 * QM_MAXE + 2) * 4;
+    static constexpr int ROOM = (228 / BLOCKS - 1) * 1024;
+    static constexpr int FIT = (ROOM - 1024 - RED_BYTES - JOIN_BYTES - TAB_BYTES) / STAGE;
+    static constexpr int STAGES = FIT < 12 ? FIT : 12;
+    static constexpr int SMEM = 1024 + STAGES * STAGE + RED_BYTES + JOIN_BYTES + TAB_BYTES;
+    static_assert(STAGES >= 2 && (3 * STAGES + 2) * 8 + 4 <= 384, "ring depth");
 };
 
 struct QuantArgs {
@@ -167,6 +207,7 @@ struct QuantArgs {
     int K, K_s;         // summed columns, routed / shared
     int ncols, ncols_s; // output columns (LINEAR M, GATE_UP d, DOWN D), routed / shared
     int nb, nb_s;       // row tiles
+    int split;          // blocks of a cluster that share a tile's columns (1, 2, 4 or 8)
     int direct;         // one token: pair j is expert topk_idx[j]'s only row
     const int32_t *topk_idx;
     const float *topk_w;
@@ -219,13 +260,17 @@ __device__ __forceinline__ bool quant_tile(int t, int routed, const QuantArgs &a
     return true;
 }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool valid) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0)
-                 : "memory");
+__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
-// This thread's arrival on `bar` once its earlier cp.async copies have landed.
-__device__ __forceinline__ void cp_async_arrive(uint64_t *bar) {
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+__device__ __forceinline__ void fence_acq_rel_cluster() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
+
+// Bulk copy of consecutive bytes into shared memory (16-byte aligned, a multiple of 16).
+__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                     smem_u32(dst)),
+                 "l"(src), "r"(bytes), "r"(smem_u32(bar))
+                 : "memory");
 }
 
 __device__ __forceinline__ void ldmatrix_x4(uint32_t addr, uint32_t (&r)[4]) {
@@ -233,53 +278,69 @@ __device__ __forceinline__ void ldmatrix_x4(uint32_t addr, uint32_t (&r)[4]) {
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                  : "r"(addr));
 }
-__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                         uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-        "{%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+// c = a b, or c += a b.
+__device__ __forceinline__ void mma_bf16(float (&c)[4], bool fresh, uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+    if (fresh)
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+            "{%10,%10,%10,%10};"
+            : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+    else
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+            "{%0,%1,%2,%3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-// Codes i and i+4 of a word as the bf16 integers -8..7.
-__device__ __forceinline__ uint32_t codes_bf16x2(uint32_t w, int i) {
-    const uint32_t v = ((w >> (4 * i)) & 0x000F000Fu) | 0x43004300u; // 128 + code
-    const __nv_bfloat162 o =
-        __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&v),
-                __nv_bfloat162(__ushort_as_bfloat16(0x4308), __ushort_as_bfloat16(0x4308))); // - 136
+template <int V> struct IntC { static constexpr int value = V; };
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t v, uint32_t c) {
+    const __nv_bfloat162 o = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&v),
+                                     *reinterpret_cast<const __nv_bfloat162 *>(&c));
     return *reinterpret_cast<const uint32_t *>(&o);
 }
+constexpr uint32_t QM_LO = 0x000F000Fu, QM_HI = 0x00F000F0u;         // codes at bits 0-3, 4-7
+constexpr uint32_t QM_X_LO = 0x5F805F80u, QM_X_HI = 0x5D805D80u;     // 2^64, 2^60 for their tokens
+constexpr float QM_OFF = -0x1p-66f; // -8 times 2^64, in units of 2^-133
+constexpr float QM_UNIT = 0x1p69f;
 
-// Maps: mW codes [E, M, K/2] bytes, box BOX x R/2 x 1, swizzled; mS scales
-// [E, K/G, M], box R/2 x SK/G x 1; the same of the shared expert (GATE_UP: its gate and
+// Maps: mW codes [E, M, K/2] bytes, box BOX x R x 1, swizzled; mS scales [E, K/G, M], box
+// R x SK/G x 1 (GATE_UP: R/2 rows); the same of the shared expert (GATE_UP: its gate and
 // up rows stacked).
-template <int KIND, int RG, int NT>
-__global__ void __launch_bounds__(QM_THREADS, 2)
+template <int KIND, int RG, int MT, int KW, int NT, int G>
+__global__ void __launch_bounds__(QM_THREADS, QmCfg<RG, MT, KW, NT, G>::BLOCKS)
     quant_product_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ CUtensorMap mS,
                          const __grid_constant__ CUtensorMap mW_s, const __grid_constant__ CUtensorMap mS_s,
                          const QuantArgs a) {
-    using C = QmCfg<RG, NT>;
-    constexpr int TT = 8 * NT, KS = C::KS, SK = C::SK, R = C::R, HALF = R / 2;
+    using C = QmCfg<RG, MT, KW, NT, G>;
+    constexpr int TT = 8 * NT, KS = C::KS, SK = C::SK, R = C::R, HALF = C::HALF;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     // ring: codes of all stages first (1024-byte aligned), then scales, then tokens
     uint8_t *ring_w = smem;
     uint8_t *ring_s = ring_w + C::STAGES * C::W_BYTES;
-    uint8_t *ring_x = ring_s + C::STAGES * C::S_BYTES;
-    float *red = reinterpret_cast<float *>(ring_x + C::STAGES * C::X_BYTES);
-    uint64_t *full = reinterpret_cast<uint64_t *>(reinterpret_cast<uint8_t *>(red) + C::RED_BYTES);
-    uint64_t *empty = full + C::STAGES;
-    volatile int *abort_flag = reinterpret_cast<volatile int *>(empty + C::STAGES);
-    int *s_tile = reinterpret_cast<int *>(reinterpret_cast<uint8_t *>(full) + 256);
+    uint8_t *ring_x = ring_s + C::STAGES * 2 * C::S_HALF;
+    uint8_t *ring_u = ring_x + C::STAGES * C::X_BYTES;
+    float *red = reinterpret_cast<float *>(ring_u + C::STAGES * C::U_BYTES);
+    float *join = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(red) + C::RED_BYTES);
+    uint64_t *full = reinterpret_cast<uint64_t *>(reinterpret_cast<uint8_t *>(join) + C::JOIN_BYTES);
+    uint64_t *empty = full + C::STAGES, *raw = empty + C::STAGES;
+    uint64_t *jfull = raw + C::STAGES, *jempty = jfull + 1;
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(jempty + 1);
+    int *s_tile = reinterpret_cast<int *>(reinterpret_cast<uint8_t *>(full) + 384);
     int *s_cnt = s_tile + QM_MAXE + 1;
 
     const int warp = warp_id(), lane = lane_id();
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::STAGES; ++s) {
-            mbar_init(&full[s], 33); // the TMA issuer and 32 lanes' copies
+            mbar_init(&full[s], 2); // the TMA issuer and the shaper
             mbar_init(&empty[s], 8);
+            mbar_init(&raw[s], 1); // the copies of the tokens
         }
+        mbar_init(jfull, 8 * a.split);
+        mbar_init(jempty, 8 * a.split);
         *abort_flag = 0;
         fence_mbar_init();
         tma_prefetch_desc(&mW);
@@ -304,7 +365,14 @@ __global__ void __launch_bounds__(QM_THREADS, 2)
             }
         }
     }
-    __syncthreads();
+    // The blocks of a cluster take the same tiles, each a share of the columns' stages.
+    const int split = KS > 1 ? a.split : 1;
+    const int rank = KS > 1 && split > 1 ? (int)cluster_ctarank() : 0;
+    const int tile0 = blockIdx.x / split, step = gridDim.x / split;
+    if (split > 1)
+        cluster_sync_all(); // every block's barriers are ready for the others' arrivals
+    else
+        __syncthreads();
     if (KIND != QUANT_LINEAR) {
         routed = (a.direct ? a.k : s_tile[a.E]) * a.nb;
         if (KIND == QUANT_GATE_UP && a.direct && blockIdx.x == 0 && threadIdx.x < a.k &&
@@ -313,40 +381,34 @@ __global__ void __launch_bounds__(QM_THREADS, 2)
     }
     const int tts = (a.N + TT - 1) / TT;
     const int total = KIND == QUANT_LINEAR ? a.nb * tts : routed + a.nb_s * tts;
-    const int gps = SK / a.G; // groups of a stage
+    constexpr int gps = SK / G; // groups of a stage
     const uint64_t limit = a.wait_limit_ns;
 
     if (warp == 8) {
         // ------------------------------ producer ------------------------------
-        const int tok = lane >> 2, ch = lane & 3; // this lane's token and 8 columns of 32
         const uint32_t stage_bytes = C::W_BYTES + 2 * HALF * gps * 2;
-        uint32_t it = 0;
+        uint32_t it = 0, s = 0, ph = 0; // stages issued, ring place and its parity
         bool ok = true;
-        for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+        for (int t = tile0; t < total && ok; t += step) {
             QuantTile c;
             if (!quant_tile<KIND, TT>(t, routed, a, s_tile, s_cnt, c)) continue;
             const int K = c.shared ? a.K_s : a.K;
-            const int nt = (c.cnt + 7) >> 3;
             const uint8_t *base = c.shared ? a.x_s : a.x;
             const size_t rb = c.shared ? a.row_bytes_s : a.row_bytes;
-            const uint8_t *src[NT];
-            bool on[NT];
-#pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                const int i = j * 8 + tok;
-                on[j] = i < c.cnt;
-                int row = c.row0 + (on[j] ? i : 0);
+            // Lane i copies token i's columns of a stage.
+            const uint8_t *src = nullptr;
+            if (lane < c.cnt) {
+                int row = c.row0 + lane;
                 if (KIND == QUANT_GATE_UP && !c.shared) row = a.direct ? 0 : a.perm_tok[row];
-                src[j] = base + (size_t)row * rb + ch * 16;
+                src = base + (size_t)row * rb;
             }
             const CUtensorMap *w = c.shared ? &mW_s : &mW, *sc = c.shared ? &mS_s : &mS;
-            // the tile's two halves: consecutive rows, or gate rows and the up rows of
-            // the same columns
+            // GATE_UP's halves are gate rows and the up rows of the same columns, a box
+            // each; otherwise the tile's rows are consecutive, one box
             const int r0 = KIND == QUANT_GATE_UP ? c.nb * HALF : c.nb * R;
-            const int r1 = KIND == QUANT_GATE_UP ? r0 + (c.shared ? a.ncols_s : a.ncols) : r0 + HALF;
+            const int r1 = r0 + (c.shared ? a.ncols_s : a.ncols);
             const int stages = (K + SK - 1) / SK;
-            for (int i = 0; i < stages; ++i, ++it) {
-                const uint32_t s = it % C::STAGES, ph = (it / C::STAGES) & 1;
+            for (int i = stages * rank / split; i < stages * (rank + 1) / split; ++i) {
                 if (lane == 0) ok = mbar_wait(&empty[s], ph ^ 1, limit, abort_flag, 401);
                 ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
                 if (!ok) break;
@@ -357,24 +419,23 @@ __global__ void __launch_bounds__(QM_THREADS, 2)
                     for (int b = 0; b < C::NBOX; ++b) {
                         const int kx = i * (SK / 2) + b * C::BOX;
                         tma_load_3d(w, &full[s], dw + b * R * C::BOX, kx, r0, c.e);
-                        tma_load_3d(w, &full[s], dw + (b * R + HALF) * C::BOX, kx, r1, c.e);
+                        if (KIND == QUANT_GATE_UP)
+                            tma_load_3d(w, &full[s], dw + (b * R + HALF) * C::BOX, kx, r1, c.e);
                     }
-                    uint8_t *ds = ring_s + s * C::S_BYTES;
+                    uint8_t *ds = ring_s + s * 2 * C::S_HALF;
                     tma_load_3d(sc, &full[s], ds, r0, i * gps, c.e);
-                    tma_load_3d(sc, &full[s], ds + C::S_BYTES / 2, r1, i * gps, c.e);
+                    if (KIND == QUANT_GATE_UP) tma_load_3d(sc, &full[s], ds + C::S_HALF, r1, i * gps, c.e);
                 }
-                const uint32_t dx = smem_u32(ring_x + s * C::X_BYTES) + lane * 16;
-#pragma unroll
-                for (int j = 0; j < NT; ++j) {
-                    if (j >= nt) break;
-#pragma unroll
-                    for (int b = 0; b < SK / 32; ++b) {
-                        const int kb = i * SK + b * 32; // K is a multiple of 32
-                        const bool v = on[j] && kb < K;
-                        cp_async16(dx + (j * (SK / 32) + b) * 512, v ? src[j] + (size_t)kb * 2 : base, v);
-                    }
+                fence_proxy_async_smem(); // the shaper wrote there before
+                const uint32_t bytes = (uint32_t)min(SK, K - i * SK) * 2;
+                if (lane == 0) mbar_arrive_expect_tx(&raw[s], bytes * c.cnt);
+                if (lane < c.cnt)
+                    bulk_load(ring_x + s * C::X_BYTES + lane * C::XLD, src + (size_t)i * SK * 2, bytes, &raw[s]);
+                ++it;
+                if (++s == C::STAGES) {
+                    s = 0;
+                    ph ^= 1;
                 }
-                cp_async_arrive(&full[s]);
             }
         }
         if (!ok && lane == 0) {
@@ -382,128 +443,246 @@ __global__ void __launch_bounds__(QM_THREADS, 2)
             const uint32_t first = it > C::STAGES ? it - C::STAGES : 0;
             for (uint32_t j = first; j < it; ++j) {
                 volatile int no_abort = 0;
-                mbar_wait(&full[j % C::STAGES], (j / C::STAGES) & 1, 10000000ull, &no_abort, 402);
+                mbar_wait(&raw[j % C::STAGES], (j / C::STAGES) & 1, 10000000ull, &no_abort, 402);
+                mbar_wait(&full[j % C::STAGES], (j / C::STAGES) & 1, 10000000ull, &no_abort, 403);
             }
         }
-        asm volatile("cp.async.wait_all;" ::: "memory");
+    } else if (warp == 9) {
+        // ------------------------------ shaper ------------------------------
+        // Brings the tokens of a stage, in place, into the order and scale of the MMA's
+        // operand (a lane's 8 columns pair as (0,4), (1,5), (2,6), (3,7)) and sums them
+        // over each unit of columns that shares a scale within a slice.
+        constexpr int LANES = C::UNIT / 8; // neighbouring lanes that hold one unit of a token
+        uint32_t s = 0, ph = 0;
+        for (int t = tile0; t < total; t += step) {
+            QuantTile c;
+            if (!quant_tile<KIND, TT>(t, routed, a, s_tile, s_cnt, c)) continue;
+            const int turns = (c.cnt * C::PIECES + 31) / 32;
+            const int K = c.shared ? a.K_s : a.K, stages = (K + SK - 1) / SK;
+            for (int i = stages * rank / split; i < stages * (rank + 1) / split; ++i) {
+                bool ok = mbar_wait(&raw[s], ph, limit, abort_flag, 405);
+                ok = __all_sync(0xffffffffu, ok);
+                if (ok) {
+                    uint8_t *xs = ring_x + s * C::X_BYTES;
+                    float *us = reinterpret_cast<float *>(ring_u + s * C::U_BYTES);
+                    // B turns of 32 pieces from turn j0 on (those past the tokens shape what
+                    // nobody reads); columns past K become zeros.
+                    auto shape = [&](auto count, int j0) {
+                        constexpr int B = decltype(count)::value;
+                        uint4 v[B], *p[B];
+                        float sum[B];
+#pragma unroll
+                        for (int j = 0; j < B; ++j) {
+                            const int at = (j0 + j) * 32 + lane, piece = at % C::PIECES;
+                            p[j] = reinterpret_cast<uint4 *>(xs + at / C::PIECES * C::XLD + piece * 16);
+                            v[j] = i * SK + piece * 8 < K ? *p[j] : make_uint4(0u, 0u, 0u, 0u);
+                        }
+#pragma unroll
+                        for (int j = 0; j < B; ++j) {
+                            float f[8];
+                            unpack_bf16x2(v[j].x, f[0], f[1]);
+                            unpack_bf16x2(v[j].y, f[2], f[3]);
+                            unpack_bf16x2(v[j].z, f[4], f[5]);
+                            unpack_bf16x2(v[j].w, f[6], f[7]);
+                            sum[j] = ((f[0] + f[1]) + (f[2] + f[3])) + ((f[4] + f[5]) + (f[6] + f[7]));
+                            *p[j] = make_uint4(mul_bf16x2(__byte_perm(v[j].x, v[j].z, 0x5410), QM_X_LO),
+                                               mul_bf16x2(__byte_perm(v[j].x, v[j].z, 0x7632), QM_X_HI),
+                                               mul_bf16x2(__byte_perm(v[j].y, v[j].w, 0x5410), QM_X_LO),
+                                               mul_bf16x2(__byte_perm(v[j].y, v[j].w, 0x7632), QM_X_HI));
+                        }
+#pragma unroll
+                        for (int d = 1; d < LANES; d <<= 1)
+#pragma unroll
+                            for (int j = 0; j < B; ++j) sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], d);
+#pragma unroll
+                        for (int j = 0; j < B; ++j) {
+                            const int at = (j0 + j) * 32 + lane;
+                            if (lane % LANES == 0)
+                                us[at % C::PIECES / LANES * TT + at / C::PIECES] = sum[j] * QM_OFF;
+                        }
+                    };
+                    if (turns == 1) {
+                        shape(IntC<1>{}, 0);
+                    } else {
+                        constexpr int B = C::TURNS < 4 ? C::TURNS : 4;
+#pragma unroll 1
+                        for (int j0 = 0; j0 < turns; j0 += B) shape(IntC<B>{}, j0);
+                    }
+                    __syncwarp();
+                }
+                if (lane == 0) mbar_arrive(&full[s]);
+                if (++s == C::STAGES) {
+                    s = 0;
+                    ph ^= 1;
+                }
+            }
+        }
     } else {
         // ------------------------------ consumers ------------------------------
         const int rg = warp / KS, ks = warp % KS;
         const int g = lane >> 2, t4 = lane & 3;
-        // This lane's ldmatrix address: row mrow of an m16 tile, 16-byte chunk (32 columns)
-        // of the slice, at the place the swizzle gives it (TMA xors the chunk with the
-        // number of the 128-byte line: the row, or half the row for 64-byte rows).
-        const int mrow = (lane & 7) + ((lane >> 3) & 1) * 8, mch = lane >> 4;
-        constexpr int CPR = C::BOX / 16;
-        const int chunk = (ks * 2) % CPR + mch, box = ks * 2 / CPR;
-        const int line = CPR == 8 ? lane & 7 : (lane & 7) >> 1;
-        const uint32_t wbase =
-            smem_u32(ring_w) + box * R * C::BOX + (uint32_t)(chunk ^ line) * 16;
-        uint32_t woff[2], soff[2];
+        // This lane's ldmatrix address: a row of the group in one half, 16-byte chunk (32
+        // columns) of the slice, at the place the swizzle gives it (TMA xors the chunk
+        // with the number of the 128-byte line: the row, or half the row for 64-byte rows).
+        constexpr int CPR = C::BOX / 16, PAIRS = KW / 64, UNIT = C::UNIT / 32;
+        const int mch = lane >> 4, line = CPR == 8 ? lane & 7 : (lane & 7) >> 1;
+        const uint32_t wbase = smem_u32(ring_w) +
+                               (uint32_t)(((lane >> 3) & 1) * HALF + rg * 8 * MT + (lane & 7)) * C::BOX;
+        uint32_t woff[PAIRS]; // 64 columns each
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int row = rg * 32 + i * 16; // first row of the m16 tile in the tile
-            woff[i] = (uint32_t)(row + mrow) * C::BOX; // halves lie one after the other
-            soff[i] = (uint32_t)(row / HALF) * (C::S_BYTES / 2) + (uint32_t)(row % HALF) * 2;
+        for (int u = 0; u < PAIRS; ++u) {
+            const int ch = ks * (KW / 32) + 2 * u;
+            woff[u] = (uint32_t)(ch / CPR) * R * C::BOX + (uint32_t)((ch % CPR + mch) ^ line) * 16;
         }
+        // this slice's first scale of the lane's row in the first half
+        constexpr int SROW = KIND == QUANT_GATE_UP ? HALF : R;                // scales of a group
+        constexpr int SHALF = KIND == QUANT_GATE_UP ? C::S_HALF / 2 : HALF;   // to the second half's
+        const uint8_t *sbase = ring_s + ((ks * KW / G) * SROW + rg * 8 * MT + g) * 2;
+        const uint8_t *xbase = ring_x + g * C::XLD + ks * KW * 2 + t4 * 16;
+        const uint8_t *ubase = ring_u + (ks * (KW / C::UNIT) * TT + 2 * t4) * 4;
         const int ctid = threadIdx.x;
-        uint32_t it = 0;
-        for (int t = blockIdx.x; t < total; t += gridDim.x) {
+        // Output (token tk, row of the tile): v, or for GATE_UP gate v and up u.
+        auto store = [&](const QuantTile &c, int tk, int row, float v, float u) {
+            const int nc = c.shared ? a.ncols_s : a.ncols;
+            const int col = c.nb * (KIND == QUANT_GATE_UP ? HALF : R) + row;
+            if (col >= nc) return;
+            const size_t at = (size_t)(c.row0 + tk) * nc + col;
+            if (KIND == QUANT_LINEAR)
+                static_cast<__nv_bfloat16 *>(a.out)[at] = __float2bfloat16_rn(v);
+            else if (KIND == QUANT_GATE_UP)
+                static_cast<__nv_bfloat16 *>(c.shared ? a.out_s : a.out)[at] =
+                    __float2bfloat16_rn(swiglu_f(v, u, a.gate_max, a.up_max));
+            else if (c.shared)
+                static_cast<float *>(a.out_s)[at] = v;
+            else
+                static_cast<float *>(a.out)[at] = v * (a.direct ? a.topk_w[c.row0] : a.w_perm[c.row0 + tk]);
+        };
+        uint32_t s = 0, ph = 0, jph = 0;
+        for (int t = tile0; t < total; t += step) {
             QuantTile c;
             if (!quant_tile<KIND, TT>(t, routed, a, s_tile, s_cnt, c)) continue;
             const int K = c.shared ? a.K_s : a.K;
             const int nt = (c.cnt + 7) >> 3;
             const int stages = (K + SK - 1) / SK;
-            float acc[2][NT][4];
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-                for (int j = 0; j < NT; ++j)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) acc[i][j][r] = 0.f;
             bool ok = true;
-            for (int st = 0; st < stages; ++st, ++it) {
-                const uint32_t s = it % C::STAGES, ph = (it / C::STAGES) & 1;
-                ok = mbar_wait(&full[s], ph, limit, abort_flag, 411);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) continue; // abort: every wait fails at once, the walk stays matched
-                uint32_t cw[2][4];
-                ldmatrix_x4(wbase + s * C::W_BYTES + woff[0], cw[0]);
-                ldmatrix_x4(wbase + s * C::W_BYTES + woff[1], cw[1]);
-                const uint8_t *xs = ring_x + s * C::X_BYTES + (ks * 2) * 512 + lane * 16;
-                const uint8_t *scs = ring_s + s * C::S_BYTES;
-                float part[2][NT][4];
+            // The tile's sums for NTT blocks of 8 tokens (blocks past nt hold anything: a
+            // column of the product depends on its own token only).
+            auto sums = [&](auto ntt) {
+                constexpr int NTT = decltype(ntt)::value;
+                float acc[MT][NTT][4];
+                uint4 xv[NTT];
+                bool on[NTT]; // this lane's token is there; absent ones are not fetched
 #pragma unroll
-                for (int h = 0; h < 2; ++h) { // 32 columns each
-                    if (h == 0 || a.G == 32) {
+                for (int j = 0; j < NTT; ++j) {
 #pragma unroll
-                        for (int i = 0; i < 2; ++i)
+                    for (int i = 0; i < MT; ++i)
 #pragma unroll
-                            for (int j = 0; j < NT; ++j)
+                        for (int r = 0; r < 4; ++r) acc[i][j][r] = 0.f;
+                    xv[j] = make_uint4(0u, 0u, 0u, 0u);
+                    on[j] = j * 8 + g < c.cnt;
+                }
+#pragma unroll 1
+                for (int st = stages * rank / split; st < stages * (rank + 1) / split; ++st) {
+                    ok = mbar_wait(&full[s], ph, limit, abort_flag, 411);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (ok) { // else abort: every wait fails at once, the walk stays matched
+                        const uint32_t ws = wbase + s * C::W_BYTES;
+                        const uint8_t *xs = xbase + s * C::X_BYTES, *scs = sbase + s * 2 * C::S_HALF;
+                        const uint8_t *us = ubase + s * C::U_BYTES;
+                        float part[MT][NTT][4];
+                        uint32_t cw[MT][4];
 #pragma unroll
-                                for (int r = 0; r < 4; ++r) part[i][j][r] = 0.f;
-                    }
-                    uint4 xv[NT];
+                        for (int b = 0; b < KW / 32; ++b) { // 32 columns each
+                            if (b % 2 == 0) {
 #pragma unroll
-                    for (int j = 0; j < NT; ++j)
-                        if (j < nt)
-                            xv[j] = *reinterpret_cast<const uint4 *>(xs + (j * (SK / 32) + h) * 512);
-#pragma unroll
-                    for (int p = 0; p < 2; ++p) {
-                        uint32_t aw[2][4];
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            aw[i][0] = codes_bf16x2(cw[i][2 * h], 2 * p);
-                            aw[i][1] = codes_bf16x2(cw[i][2 * h + 1], 2 * p);
-                            aw[i][2] = codes_bf16x2(cw[i][2 * h], 2 * p + 1);
-                            aw[i][3] = codes_bf16x2(cw[i][2 * h + 1], 2 * p + 1);
-                        }
-#pragma unroll
-                        for (int j = 0; j < NT; ++j) {
-                            if (j < nt) {
-                                const uint32_t lo = p ? xv[j].y : xv[j].x, hi = p ? xv[j].w : xv[j].z;
-                                const uint32_t b0 = __byte_perm(lo, hi, 0x5410);
-                                const uint32_t b1 = __byte_perm(lo, hi, 0x7632);
-#pragma unroll
-                                for (int i = 0; i < 2; ++i)
-                                    mma_bf16(part[i][j], aw[i][0], aw[i][1], aw[i][2], aw[i][3], b0, b1);
+                                for (int i = 0; i < MT; ++i) ldmatrix_x4(ws + woff[b / 2] + i * 8 * C::BOX, cw[i]);
                             }
-                        }
-                    }
-                    if (h == 1 || a.G == 32) {
-                        const int gi = (ks * 64 + h * 32) / a.G; // group in the stage
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const __nv_bfloat16 *sp =
-                                reinterpret_cast<const __nv_bfloat16 *>(scs + soff[i]) + gi * HALF;
-                            const float s0 = __bfloat162float(sp[g]), s1 = __bfloat162float(sp[g + 8]);
+                            for (int j = 0; j < NTT; ++j)
+                                if (on[j])
+                                    xv[j] = *reinterpret_cast<const uint4 *>(xs + j * 8 * C::XLD + b * 64);
 #pragma unroll
-                            for (int j = 0; j < NT; ++j) {
-                                if (j < nt) {
-                                    acc[i][j][0] = fmaf(s0, part[i][j][0], acc[i][j][0]);
-                                    acc[i][j][1] = fmaf(s0, part[i][j][1], acc[i][j][1]);
-                                    acc[i][j][2] = fmaf(s1, part[i][j][2], acc[i][j][2]);
-                                    acc[i][j][3] = fmaf(s1, part[i][j][3], acc[i][j][3]);
+                            for (int p = 0; p < 2; ++p)
+#pragma unroll
+                                for (int i = 0; i < MT; ++i) {
+                                    const uint32_t r0 = cw[i][2 * (b % 2)] >> (8 * p);
+                                    const uint32_t r1 = cw[i][2 * (b % 2) + 1] >> (8 * p);
+#pragma unroll
+                                    for (int j = 0; j < NTT; ++j)
+                                        mma_bf16(part[i][j], b % UNIT == 0 && p == 0, r0 & QM_LO, r1 & QM_LO,
+                                                 r0 & QM_HI, r1 & QM_HI, p ? xv[j].z : xv[j].x,
+                                                 p ? xv[j].w : xv[j].y);
+                                }
+                            if ((b + 1) % UNIT == 0) { // the group, or its part here, ends
+                                float2 off[NTT]; // of tokens 2 t4, 2 t4 + 1
+#pragma unroll
+                                for (int j = 0; j < NTT; ++j)
+                                    off[j] = *reinterpret_cast<const float2 *>(us + ((b / UNIT) * TT + j * 8) * 4);
+#pragma unroll
+                                for (int i = 0; i < MT; ++i) {
+                                    const __nv_bfloat16 *sp =
+                                        reinterpret_cast<const __nv_bfloat16 *>(scs) + (b * 32 / G) * SROW + i * 8;
+                                    const float s0 = __bfloat162float(sp[0]) * QM_UNIT;
+                                    const float s1 = __bfloat162float(sp[SHALF]) * QM_UNIT;
+#pragma unroll
+                                    for (int j = 0; j < NTT; ++j) {
+                                        acc[i][j][0] = fmaf(s0, part[i][j][0] + off[j].x, acc[i][j][0]);
+                                        acc[i][j][1] = fmaf(s0, part[i][j][1] + off[j].y, acc[i][j][1]);
+                                        acc[i][j][2] = fmaf(s1, part[i][j][2] + off[j].x, acc[i][j][2]);
+                                        acc[i][j][3] = fmaf(s1, part[i][j][3] + off[j].y, acc[i][j][3]);
+                                    }
                                 }
                             }
                         }
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&empty[s]);
+                    }
+                    if (++s == C::STAGES) {
+                        s = 0;
+                        ph ^= 1;
                     }
                 }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&empty[s]);
-            }
-            named_bar_sync(1, QM_CONSUMERS); // the last tile's sums have been read
+                if (KS == 1) {
+                    if (!ok) return;
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+                    for (int j = 0; j < NTT; ++j)
 #pragma unroll
-                for (int j = 0; j < NT; ++j)
-                    if (j < nt) {
-                        float *d = red + (ks * TT + j * 8 + 2 * t4) * C::LD + rg * 32 + i * 16 + g;
-                        d[0] = acc[i][j][0];
-                        d[C::LD] = acc[i][j][1];
-                        d[8] = acc[i][j][2];
-                        d[C::LD + 8] = acc[i][j][3];
-                    }
+                        for (int r = 0; r < 2; ++r) {
+                            const int tk = j * 8 + 2 * t4 + r;
+                            if (tk < c.cnt) {
+#pragma unroll
+                                for (int i = 0; i < MT; ++i) {
+                                    const int row = (rg * MT + i) * 8 + g;
+                                    if (KIND == QUANT_GATE_UP) {
+                                        store(c, tk, row, acc[i][j][r], acc[i][j][2 + r]);
+                                    } else {
+                                        store(c, tk, row, acc[i][j][r], 0.f);
+                                        store(c, tk, HALF + row, acc[i][j][2 + r], 0.f);
+                                    }
+                                }
+                            }
+                        }
+                } else {
+                    named_bar_sync(1, QM_CONSUMERS); // the last tile's sums have been read
+#pragma unroll
+                    for (int i = 0; i < MT; ++i)
+#pragma unroll
+                        for (int j = 0; j < NTT; ++j) {
+                            float *d = red + (ks * TT + j * 8 + 2 * t4) * C::LD + (rg * MT + i) * 8 + g;
+                            d[0] = acc[i][j][0];
+                            d[C::LD] = acc[i][j][1];
+                            d[HALF] = acc[i][j][2];
+                            d[C::LD + HALF] = acc[i][j][3];
+                        }
+                }
+            };
+            if (NT == 1 || nt == 1)
+                sums(IntC<1>{});
+            else if (NT == 2 || nt == 2)
+                sums(IntC<NT < 2 ? NT : 2>{});
+            else
+                sums(IntC<NT>{});
+            if (KS == 1) continue;
             named_bar_sync(1, QM_CONSUMERS);
             if (!ok) continue;
             auto sum = [&](int tk, int row) {
@@ -512,31 +691,51 @@ __global__ void __launch_bounds__(QM_THREADS, 2)
                 for (int q = 1; q < KS; ++q) v += red[(q * TT + tk) * C::LD + row];
                 return v;
             };
-            const int nc = c.shared ? a.ncols_s : a.ncols;
-            if (KIND == QUANT_GATE_UP) {
-                __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(c.shared ? a.out_s : a.out);
-                for (int i = ctid; i < c.cnt * HALF; i += QM_CONSUMERS) {
-                    const int tk = i / HALF, f = i % HALF, col = c.nb * HALF + f;
-                    if (col < nc)
-                        out[(size_t)(c.row0 + tk) * nc + col] = __float2bfloat16_rn(
-                            swiglu_f(sum(tk, f), sum(tk, HALF + f), a.gate_max, a.up_max));
+            constexpr int OUT = KIND == QUANT_GATE_UP ? HALF : R;
+            if (split == 1) {
+                for (int i = ctid; i < c.cnt * OUT; i += QM_CONSUMERS) {
+                    const int tk = i / OUT, row = i % OUT;
+                    store(c, tk, row, sum(tk, row), KIND == QUANT_GATE_UP ? sum(tk, HALF + row) : 0.f);
                 }
-            } else {
-                for (int i = ctid; i < c.cnt * R; i += QM_CONSUMERS) {
-                    const int tk = i / R, f = i % R, col = c.nb * R + f;
-                    if (col >= nc) continue;
-                    const size_t at = (size_t)(c.row0 + tk) * nc + col;
-                    const float v = sum(tk, f);
-                    if (KIND == QUANT_LINEAR)
-                        static_cast<__nv_bfloat16 *>(a.out)[at] = __float2bfloat16_rn(v);
-                    else if (c.shared)
-                        static_cast<float *>(a.out_s)[at] = v;
-                    else
-                        static_cast<float *>(a.out)[at] =
-                            v * (a.direct ? a.topk_w[c.row0] : a.w_perm[c.row0 + tk]);
-                }
+                continue;
             }
+            // Each block of the cluster finishes HALF / split rows of either half: the
+            // others' sums come into its `join` [block][token][2][rows], and are added in
+            // the blocks' order.
+            const int own = HALF / split;
+            ok = mbar_wait_cl(jempty, jph ^ 1, limit, abort_flag, 412); // all have read the last tile's
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) continue;
+            for (int i = ctid; i < c.cnt * R; i += QM_CONSUMERS) {
+                const int tk = i / R, row = i % R, f = row % HALF;
+                st_cluster_f32(mapa_shared(smem_u32(join + (rank * TT + tk) * 2 * own + (row / HALF) * own + f % own),
+                                           f / own),
+                               sum(tk, row));
+            }
+            fence_acq_rel_cluster();
+            __syncwarp();
+            if (lane < split) mbar_arrive_remote(mapa_shared(smem_u32(jfull), lane));
+            ok = mbar_wait_cl(jfull, jph, limit, abort_flag, 413);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) continue;
+            auto joined = [&](int tk, int at) {
+                float v = join[tk * 2 * own + at];
+                for (int q = 1; q < split; ++q) v += join[(q * TT + tk) * 2 * own + at];
+                return v;
+            };
+            const int out = KIND == QUANT_GATE_UP ? own : 2 * own;
+            for (int i = ctid; i < c.cnt * out; i += QM_CONSUMERS) {
+                const int tk = i / out, at = i % out, row = (at / own) * HALF + rank * own + at % own;
+                store(c, tk, row, joined(tk, at), KIND == QUANT_GATE_UP ? joined(tk, own + at) : 0.f);
+            }
+            __syncwarp();
+            if (lane < split) mbar_arrive_remote(mapa_shared(smem_u32(jempty), lane));
+            jph ^= 1;
         }
+    }
+    if (split > 1) {
+        __syncwarp();
+        cluster_sync_all(); // no block leaves while another may still write to it
     }
 }
 

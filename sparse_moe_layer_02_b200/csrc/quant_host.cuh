@@ -15,20 +15,22 @@ bool quant_shape_ok(int E, int M, int K, int G) {
            K <= (1 << 24) && K % G == 0;
 }
 
-// Maps of the codes and scales of E matrices [M, K] for tiles of C::R rows.
-template <typename C>
+// Maps of the codes and scales of E matrices [M, K] for the tiles of a configuration.
+template <int RG, int MT, int KW>
 bool make_quant_maps(CUtensorMap *mW, CUtensorMap *mS, const void *q, const void *s, int E, int M, int K,
-                     int G) {
+                     int G, bool halves) {
+    using C = QmCfg<RG, MT, KW, 1, 32>; // the boxes do not depend on NT and G
     auto fn = encode_fn();
     if (!fn) return false;
     const cuuint64_t half = (cuuint64_t)K / 2, groups = (cuuint64_t)K / G;
     cuuint32_t estr[3] = {1, 1, 1};
     cuuint64_t wd[3] = {half, (cuuint64_t)M, (cuuint64_t)E};
     cuuint64_t ws[2] = {half, half * M};
-    cuuint32_t wb[3] = {C::BOX, C::R / 2, 1};
+    const cuuint32_t rows = halves ? C::HALF : C::R;
+    cuuint32_t wb[3] = {C::BOX, rows, 1};
     cuuint64_t sd[3] = {(cuuint64_t)M, groups, (cuuint64_t)E};
     cuuint64_t ss[2] = {(cuuint64_t)M * 2, (cuuint64_t)M * 2 * groups};
-    cuuint32_t sb[3] = {C::R / 2, (cuuint32_t)(C::SK / G), 1};
+    cuuint32_t sb[3] = {rows, (cuuint32_t)(C::SK / G), 1};
     return fn(mW, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(q), wd, ws, wb, estr,
               CU_TENSOR_MAP_INTERLEAVE_NONE,
               C::BOX == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
@@ -38,46 +40,75 @@ bool make_quant_maps(CUtensorMap *mW, CUtensorMap *mS, const void *q, const void
               CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int KIND, int RG, int NT>
-int launch_quant(const CUtensorMap &mW, const CUtensorMap &mS, const CUtensorMap &mW_s,
+// Blocks that share a tile: as many as still run all at once (clusters do not fill every
+// place, so two thirds of them are counted on), each with two stages of columns at least.
+// A block alone on an SM has too few warps to hide its latencies: 12288 x 6144, one token
+// (96 tiles), MEASURED.  Sharing when the tiles already take several rounds costs: the
+// exchange (2 us) then stalls the next tile's reading.
+int quant_split(size_t tiles, size_t slots, int stages) {
+    int best = 1;
+    for (int c = 2; c <= 8 && tiles * c * 3 <= slots * 2 && stages >= 2 * c; c *= 2) best = c;
+    return best;
+}
+
+template <int KIND, int RG, int MT, int KW, int NT, int G>
+int launch_quant_g(const CUtensorMap &mW, const CUtensorMap &mS, const CUtensorMap &mW_s,
                  const CUtensorMap &mS_s, const QuantArgs &a, size_t tiles, DeviceInfo *info,
                  cudaStream_t st) {
-    using C = QmCfg<RG, NT>;
+    using C = QmCfg<RG, MT, KW, NT, G>;
     static bool attr_set[kMaxDevices] = {}; // function attributes are set per device
     const int dev = current_device_index();
     if (dev < 0) return MOE_ERR_CUDA;
     {
         std::lock_guard<std::mutex> lk(g_mu);
         if (!attr_set[dev]) {
-            if (cudaFuncSetAttribute(quant_product_kernel<KIND, RG, NT>,
+            if (cudaFuncSetAttribute(quant_product_kernel<KIND, RG, MT, KW, NT, G>,
                                      cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
                 return MOE_ERR_CUDA;
             attr_set[dev] = true;
         }
     }
+    const size_t slots = (size_t)info->sms * C::BLOCKS;
+    QuantArgs b = a;
+    b.split = C::KS > 1 ? quant_split(tiles, slots, (std::max(a.K, a.K_s) + C::SK - 1) / C::SK) : 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)std::min<size_t>(tiles, (size_t)info->sms * 2), 1, 1);
+    cfg.gridDim = dim3((unsigned)(std::min<size_t>(tiles, slots / b.split) * b.split), 1, 1);
     cfg.blockDim = dim3(QM_THREADS, 1, 1);
     cfg.dynamicSmemBytes = C::SMEM;
     cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = b.split;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (launch_ex(cfg, quant_product_kernel<KIND, RG, NT>, mW, mS, mW_s, mS_s, a) != cudaSuccess)
+    cfg.numAttrs = 2;
+    if (launch_ex(cfg, quant_product_kernel<KIND, RG, MT, KW, NT, G>, mW, mS, mW_s, mS_s, b) != cudaSuccess)
         return MOE_ERR_CUDA;
     return launch_status();
 }
 
-template <int RG, int NT>
+template <int KIND, int RG, int MT, int KW, int NT>
+int launch_quant(const CUtensorMap &mW, const CUtensorMap &mS, const CUtensorMap &mW_s,
+                 const CUtensorMap &mS_s, const QuantArgs &a, size_t tiles, DeviceInfo *info,
+                 cudaStream_t st) {
+    switch (a.G) {
+    case 32: return launch_quant_g<KIND, RG, MT, KW, NT, 32>(mW, mS, mW_s, mS_s, a, tiles, info, st);
+    case 64: return launch_quant_g<KIND, RG, MT, KW, NT, 64>(mW, mS, mW_s, mS_s, a, tiles, info, st);
+    default: return launch_quant_g<KIND, RG, MT, KW, NT, 128>(mW, mS, mW_s, mS_s, a, tiles, info, st);
+    }
+}
+
+template <int RG, int MT, int KW, int NT>
 int linear_quant_t(const void *q, const void *s, QuantArgs a, DeviceInfo *info, cudaStream_t st) {
-    using C = QmCfg<RG, NT>;
+    constexpr int R = 16 * MT * RG;
     CUtensorMap mW, mS;
-    if (!make_quant_maps<C>(&mW, &mS, q, s, 1, a.ncols, a.K, a.G)) return MOE_ERR_CUDA;
-    a.nb = (a.ncols + C::R - 1) / C::R;
+    if (!make_quant_maps<RG, MT, KW>(&mW, &mS, q, s, 1, a.ncols, a.K, a.G, false)) return MOE_ERR_CUDA;
+    a.nb = (a.ncols + R - 1) / R;
     const size_t tiles = (size_t)a.nb * ((a.N + 8 * NT - 1) / (8 * NT));
-    return launch_quant<QUANT_LINEAR, RG, NT>(mW, mS, mW, mS, a, tiles, info, st);
+    return launch_quant<QUANT_LINEAR, RG, MT, KW, NT>(mW, mS, mW, mS, a, tiles, info, st);
 }
 
 // ---- the layer ----
@@ -135,33 +166,33 @@ struct QuantLayer {
     int D, d, d_sh;
 };
 
-template <int RG, int NT>
+template <int RG, int MT, int KW, int NT>
 int quant_layer_t(const QuantLayer &w, QuantArgs a, const void *x, uint8_t *ws, const QuantWs &W,
                   DeviceInfo *info, Profiler &prof, cudaStream_t st) {
-    using C = QmCfg<RG, NT>;
+    constexpr int R = 16 * MT * RG;
     const int tt_s = (a.N + 8 * NT - 1) / (8 * NT);
     const size_t tt_r = W.direct ? (size_t)a.k : W.rows_max / (8 * NT) + 1;
     CUtensorMap mW, mS, mWs, mSs;
     // gate and up rows, SwiGLU
-    if (!make_quant_maps<C>(&mW, &mS, w.gu, w.gu_s, a.E, 2 * w.d, w.D, a.G) ||
-        !make_quant_maps<C>(&mWs, &mSs, w.sgu, w.sgu_s, 1, 2 * w.d_sh, w.D, a.G))
+    if (!make_quant_maps<RG, MT, KW>(&mW, &mS, w.gu, w.gu_s, a.E, 2 * w.d, w.D, a.G, true) ||
+        !make_quant_maps<RG, MT, KW>(&mWs, &mSs, w.sgu, w.sgu_s, 1, 2 * w.d_sh, w.D, a.G, true))
         return MOE_ERR_CUDA;
     a.x = a.x_s = static_cast<const uint8_t *>(x);
     a.row_bytes = a.row_bytes_s = w.D * 2;
     a.K = a.K_s = w.D;
     a.ncols = w.d;
     a.ncols_s = w.d_sh;
-    a.nb = (w.d + C::R / 2 - 1) / (C::R / 2);
-    a.nb_s = (w.d_sh + C::R / 2 - 1) / (C::R / 2);
+    a.nb = (w.d + R / 2 - 1) / (R / 2);
+    a.nb_s = (w.d_sh + R / 2 - 1) / (R / 2);
     a.out = ws + W.h;
     a.out_s = ws + W.h_s;
-    int rc = launch_quant<QUANT_GATE_UP, RG, NT>(mW, mS, mWs, mSs, a, tt_r * a.nb + (size_t)tt_s * a.nb_s,
+    int rc = launch_quant<QUANT_GATE_UP, RG, MT, KW, NT>(mW, mS, mWs, mSs, a, tt_r * a.nb + (size_t)tt_s * a.nb_s,
                                                  info, st);
     if (rc != MOE_OK) return rc;
     prof.mark();
     // down
-    if (!make_quant_maps<C>(&mW, &mS, w.dn, w.dn_s, a.E, w.D, w.d, a.G) ||
-        !make_quant_maps<C>(&mWs, &mSs, w.sdn, w.sdn_s, 1, w.D, w.d_sh, a.G))
+    if (!make_quant_maps<RG, MT, KW>(&mW, &mS, w.dn, w.dn_s, a.E, w.D, w.d, a.G, false) ||
+        !make_quant_maps<RG, MT, KW>(&mWs, &mSs, w.sdn, w.sdn_s, 1, w.D, w.d_sh, a.G, false))
         return MOE_ERR_CUDA;
     a.x = ws + W.h;
     a.x_s = ws + W.h_s;
@@ -170,10 +201,10 @@ int quant_layer_t(const QuantLayer &w, QuantArgs a, const void *x, uint8_t *ws, 
     a.K = w.d;
     a.K_s = w.d_sh;
     a.ncols = a.ncols_s = w.D;
-    a.nb = a.nb_s = (w.D + C::R - 1) / C::R;
+    a.nb = a.nb_s = (w.D + R - 1) / R;
     a.out = ws + W.slot;
     a.out_s = ws + W.osh;
-    rc = launch_quant<QUANT_DOWN, RG, NT>(mW, mS, mWs, mSs, a, tt_r * a.nb + (size_t)tt_s * a.nb_s, info, st);
+    rc = launch_quant<QUANT_DOWN, RG, MT, KW, NT>(mW, mS, mWs, mSs, a, tt_r * a.nb + (size_t)tt_s * a.nb_s, info, st);
     if (rc == MOE_OK) prof.mark();
     return rc;
 }
@@ -206,7 +237,7 @@ int moe_dequantize(const void *q, const void *scales, int E, int M, int K, int g
     int rc = current_device_info(&dev);
     if (rc != MOE_OK) return rc;
     if (dev->major != 10) return MOE_ERR_NO_DEVICE;
-    const dim3 grid((K + QZ_COLS - 1) / QZ_COLS, (M + QZ_ROWS - 1) / QZ_ROWS, E);
+    const dim3 grid((K + QZ_COLS - 1) / QZ_COLS, (M + DQ_ROWS - 1) / DQ_ROWS, E);
     dequantize_kernel<<<grid, QZ_THREADS, 0, static_cast<cudaStream_t>(stream)>>>(
         static_cast<const uint8_t *>(q), static_cast<const __nv_bfloat16 *>(scales),
         static_cast<__nv_bfloat16 *>(W), M, K, group);
@@ -235,12 +266,10 @@ int moe_linear_quant(const void *x, const void *q, const void *scales, int N, in
     a.out = y;
     a.wait_limit_ns = g_wait_limit_ns;
     if (N <= 8) {
-        // Few rows: 32-row tiles, so that more SMs have one.
-        if ((size_t)M < (size_t)64 * 2 * dev->sms) return linear_quant_t<1, 1>(q, scales, a, dev, st);
-        return linear_quant_t<2, 1>(q, scales, a, dev, st);
+        return linear_quant_t<4, 2, 128, 1>(q, scales, a, dev, st);
     }
-    if (N <= 16) return linear_quant_t<2, 2>(q, scales, a, dev, st);
-    return linear_quant_t<4, 4>(q, scales, a, dev, st);
+    if (N <= 16) return linear_quant_t<4, 2, 128, 2>(q, scales, a, dev, st);
+    return linear_quant_t<8, 2, 128, 4>(q, scales, a, dev, st);
 }
 
 size_t moe_forward_quant_workspace(int N, int D, int E, int d_moe, int d_sh, int k) {
@@ -324,9 +353,10 @@ int moe_forward_quant(const void *x, const void *gate_up, const void *gate_up_sc
     }
     const QuantLayer w = {gate_up, gate_up_scales, down, down_scales, sh_gate_up, sh_gate_up_scales,
                           sh_down, sh_down_scales, D, d_moe, d_sh};
-    rc = W.tile_rows == 8    ? quant_layer_t<2, 1>(w, a, x, ws, W, dev, prof, st)
-         : W.tile_rows == 16 ? quant_layer_t<2, 2>(w, a, x, ws, W, dev, prof, st)
-                             : quant_layer_t<4, 4>(w, a, x, ws, W, dev, prof, st);
+    rc = W.direct            ? quant_layer_t<4, 2, 128, 1>(w, a, x, ws, W, dev, prof, st)
+         : W.tile_rows == 8  ? quant_layer_t<8, 2, 128, 1>(w, a, x, ws, W, dev, prof, st)
+         : W.tile_rows == 16 ? quant_layer_t<8, 2, 128, 2>(w, a, x, ws, W, dev, prof, st)
+                             : quant_layer_t<8, 2, 128, 4>(w, a, x, ws, W, dev, prof, st);
     if (rc != MOE_OK) return rc;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(N, (D + 1023) / 1024, 1);

@@ -10,43 +10,63 @@ on that device's current stream unless a stream is given, and needs all tensors 
 
 from __future__ import annotations
 
-import contextlib
-
 import torch
 
-from . import _check, _dev, _dt, load_library
+from . import MOE_BF16, MOE_F32, _check, load_library
 
 __all__ = ["moe_grouped_linear", "moe_grouped_linear_dgrad", "moe_grouped_linear_wgrad"]
 
 
-def _device(first, *others):
-    """The device all tensors are on, as an index."""
-    if not isinstance(first, torch.Tensor) or not first.is_cuda:
-        raise ValueError("the tensors must be CUDA tensors")
-    dev = first.device
-    for t in others:
-        if t.device != dev:
-            raise ValueError("the tensors must be on one device (%s and %s)" % (dev, t.device))
-    return dev.index
+# The calls themselves take a few microseconds on the GPU at decode sizes, so what a binding
+# spends before the launch is kept small: a tensor's device is read as an index, the current
+# stream as a raw handle, and the device is switched only where it differs.
+_current_stream = torch._C._cuda_getCurrentRawStream
+_DTYPES = {torch.bfloat16: MOE_BF16, torch.float32: MOE_F32}
 
 
-def _on(dev: int):
-    """Makes dev the current device where it is not."""
-    return contextlib.nullcontext() if dev == torch.cuda.current_device() else torch.cuda.device(dev)
+def _dt(t):
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        raise ValueError("unsupported dtype %s (float32 or bfloat16)" % t.dtype)
+    return code
 
 
-def _stream_on(dev: int, stream) -> int:
+def _device(*tensors):
+    """The index of the device all tensors are on; they must be contiguous."""
+    dev = -2
+    for t in tensors:
+        if not isinstance(t, torch.Tensor) or t.get_device() != dev:
+            if dev != -2 or not isinstance(t, torch.Tensor) or not t.is_cuda:
+                raise ValueError("the tensors must be CUDA tensors on one device")
+            dev = t.get_device()
+        if not t.is_contiguous():
+            raise ValueError("the tensors must be contiguous")
+    return dev
+
+
+def _call(name, dev, stream, *args):
+    """One library call on device dev, with the stream as its last argument."""
+    f = getattr(load_library(), name)
     if stream is None:
-        return torch.cuda.current_stream(dev).cuda_stream
-    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+        stream = _current_stream(dev)
+    elif isinstance(stream, torch.cuda.Stream):
+        stream = stream.cuda_stream
+    if dev == torch.cuda.current_device():
+        rc = f(*args, stream)
+    else:
+        with torch.cuda.device(dev):
+            rc = f(*args, stream)
+    if rc:
+        _check(rc, name)
 
 
-def _out(t, shape, dtype, dev, name):
-    """An output the caller gave, checked, or a new one (unset)."""
+def _out(t, shape, dtype, like, name):
+    """An output the caller gave, checked, or a new one (unset) on the device of `like`."""
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=torch.device("cuda", dev))
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device.index != dev:
-        raise ValueError("%s must be %s %s on the inputs' device" % (name, list(shape), dtype))
+        return like.new_empty(shape, dtype=dtype)
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.get_device() != like.get_device() \
+            or not t.is_contiguous():
+        raise ValueError("%s must be contiguous, %s %s on the inputs' device" % (name, list(shape), dtype))
     return t
 
 
@@ -69,11 +89,9 @@ def _linear(x, W, offsets, y, stream):
     (rows, K), (E, M, _) = x.shape, W.shape
     _check_offsets(offsets, E)
     rest = int(y is None)
-    y = _out(y, (rows, M), x.dtype, dev, "y")
-    with _on(dev):
-        _check(load_library().moe_grouped_linear(
-            _dev(x, "x"), _dev(W, "W"), _dev(offsets, "offsets"), rows, E, M, K, _dt(x),
-            _dev(y, "y"), rest, _stream_on(dev, stream)), "moe_grouped_linear")
+    y = _out(y, (rows, M), x.dtype, x, "y")
+    _call("moe_grouped_linear", dev, stream, x.data_ptr(), W.data_ptr(), offsets.data_ptr(), rows,
+          E, M, K, _dt(x), y.data_ptr(), rest)
     return y
 
 
@@ -117,11 +135,9 @@ def moe_grouped_linear_dgrad(dy, W, offsets, dx=None, stream=None):
     rows, (E, M, K) = dy.shape[0], W.shape
     _check_offsets(offsets, E)
     rest = int(dx is None)
-    dx = _out(dx, (rows, K), dy.dtype, dev, "dx")
-    with _on(dev):
-        _check(load_library().moe_grouped_linear_dgrad(
-            _dev(dy, "dy"), _dev(W, "W"), _dev(offsets, "offsets"), rows, E, M, K, _dt(dy),
-            _dev(dx, "dx"), rest, _stream_on(dev, stream)), "moe_grouped_linear_dgrad")
+    dx = _out(dx, (rows, K), dy.dtype, dy, "dx")
+    _call("moe_grouped_linear_dgrad", dev, stream, dy.data_ptr(), W.data_ptr(), offsets.data_ptr(),
+          rows, E, M, K, _dt(dy), dx.data_ptr(), rest)
     return dx
 
 
@@ -134,9 +150,7 @@ def moe_grouped_linear_wgrad(dy, x, offsets, dW=None, stream=None):
     _same_type(dy, x)
     (rows, M), K, E = dy.shape, x.shape[1], offsets.shape[0] - 1
     _check_offsets(offsets, E)
-    dW = _out(dW, (E, M, K), dy.dtype, dev, "dW")
-    with _on(dev):
-        _check(load_library().moe_grouped_linear_wgrad(
-            _dev(dy, "dy"), _dev(x, "x"), _dev(offsets, "offsets"), rows, E, M, K, _dt(dy),
-            _dev(dW, "dW"), _stream_on(dev, stream)), "moe_grouped_linear_wgrad")
+    dW = _out(dW, (E, M, K), dy.dtype, dy, "dW")
+    _call("moe_grouped_linear_wgrad", dev, stream, dy.data_ptr(), x.data_ptr(), offsets.data_ptr(),
+          rows, E, M, K, _dt(dy), dW.data_ptr())
     return dW

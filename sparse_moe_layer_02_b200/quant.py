@@ -16,8 +16,8 @@ from __future__ import annotations
 
 import torch
 
-from . import _check, _dev, load_library
-from .products import _device, _on, _out, _stream_on
+from . import load_library
+from .products import _call, _device, _out
 
 __all__ = ["moe_quantize", "moe_dequantize", "moe_linear_quant", "moe_forward_quant",
            "moe_forward_quant_workspace"]
@@ -27,12 +27,12 @@ def _pair(q, scales, lead, name):
     """(M, K, group) of 4-bit weights with `lead` leading dimensions."""
     if q.dtype != torch.uint8 or scales.dtype != torch.bfloat16:
         raise ValueError("%s must be (uint8 codes, bfloat16 scales)" % name)
-    if q.dim() != lead + 2 or scales.dim() != lead + 2 or q.shape[:lead] != scales.shape[:lead]:
-        raise ValueError("%s: codes [.., M, K/2] and scales [.., K/group, M] do not agree" % name)
-    M, K, groups = q.shape[-2], 2 * q.shape[-1], scales.shape[-2]
-    if scales.shape[-1] != M or groups == 0 or K % groups:
-        raise ValueError("%s: codes [.., M, K/2] and scales [.., K/group, M] do not agree" % name)
-    return M, K, K // groups
+    qs, ss = q.shape, scales.shape
+    if len(qs) == lead + 2 and len(ss) == lead + 2 and qs[:lead] == ss[:lead]:
+        M, K, groups = qs[lead], 2 * qs[lead + 1], ss[lead]
+        if ss[lead + 1] == M and groups and not K % groups:
+            return M, K, K // groups
+    raise ValueError("%s: codes [.., M, K/2] and scales [.., K/group, M] do not agree" % name)
 
 
 def moe_quantize(W, group: int = 128, q=None, scales=None, stream=None):
@@ -43,13 +43,10 @@ def moe_quantize(W, group: int = 128, q=None, scales=None, stream=None):
     lead, (M, K) = tuple(W.shape[:-2]), W.shape[-2:]
     if group not in (32, 64, 128) or K % group:
         raise ValueError("group must be 32, 64 or 128 and divide K")
-    q = _out(q, lead + (M, K // 2), torch.uint8, dev, "q")
-    scales = _out(scales, lead + (K // group, M), torch.bfloat16, dev, "scales")
+    q = _out(q, lead + (M, K // 2), torch.uint8, W, "q")
+    scales = _out(scales, lead + (K // group, M), torch.bfloat16, W, "scales")
     E = W.numel() // (M * K) if M * K else 0
-    with _on(dev):
-        _check(load_library().moe_quantize(_dev(W, "W"), E, M, K, group, _dev(q, "q"),
-                                           _dev(scales, "scales"), _stream_on(dev, stream)),
-               "moe_quantize")
+    _call("moe_quantize", dev, stream, W.data_ptr(), E, M, K, group, q.data_ptr(), scales.data_ptr())
     return q, scales
 
 
@@ -57,12 +54,9 @@ def moe_dequantize(q, scales, W=None, stream=None):
     """The bf16 values [..., M, K] of 4-bit weights."""
     M, K, group = _pair(q, scales, q.dim() - 2, "the weights")
     dev = _device(q, scales)
-    W = _out(W, tuple(q.shape[:-2]) + (M, K), torch.bfloat16, dev, "W")
+    W = _out(W, tuple(q.shape[:-2]) + (M, K), torch.bfloat16, q, "W")
     E = W.numel() // (M * K) if M * K else 0
-    with _on(dev):
-        _check(load_library().moe_dequantize(_dev(q, "q"), _dev(scales, "scales"), E, M, K, group,
-                                             _dev(W, "W"), _stream_on(dev, stream)),
-               "moe_dequantize")
+    _call("moe_dequantize", dev, stream, q.data_ptr(), scales.data_ptr(), E, M, K, group, W.data_ptr())
     return W
 
 
@@ -73,11 +67,9 @@ def moe_linear_quant(x, q, scales, y=None, stream=None):
         raise ValueError("x must be bfloat16 [N, K]")
     dev = _device(x, q, scales)
     N = x.shape[0]
-    y = _out(y, (N, M), torch.bfloat16, dev, "y")
-    with _on(dev):
-        _check(load_library().moe_linear_quant(_dev(x, "x"), _dev(q, "q"), _dev(scales, "scales"),
-                                               N, M, K, group, _dev(y, "y"),
-                                               _stream_on(dev, stream)), "moe_linear_quant")
+    y = _out(y, (N, M), torch.bfloat16, x, "y")
+    _call("moe_linear_quant", dev, stream, x.data_ptr(), q.data_ptr(), scales.data_ptr(), N, M, K,
+          group, y.data_ptr())
     return y
 
 
@@ -110,22 +102,17 @@ def moe_forward_quant(x, gate_up, down, sh_gate_up, sh_down, topk_idx, topk_w, y
         raise ValueError("topk_idx must be int32 and topk_w float32, both [N, k]")
     k = topk_idx.shape[1]
     dev = _device(x, *gate_up, *down, *sh_gate_up, *sh_down, topk_idx, topk_w)
-    y = _out(y, (N, D), torch.bfloat16, dev, "y")
+    y = _out(y, (N, D), torch.bfloat16, x, "y")
     if workspace is None:
-        workspace = torch.empty(max(moe_forward_quant_workspace(N, D, E, d, d_sh, k), 256),
-                                dtype=torch.uint8, device=x.device)
-    elif workspace.device != x.device:
-        raise ValueError("the workspace must be on the inputs' device")
+        workspace = x.new_empty(max(moe_forward_quant_workspace(N, D, E, d, d_sh, k), 256),
+                                dtype=torch.uint8)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError("the workspace must be contiguous, on the inputs' device")
     inf = float("inf")
-    with _on(dev):
-        _check(load_library().moe_forward_quant(
-            _dev(x, "x"), _dev(gate_up[0], "gate_up"), _dev(gate_up[1], "gate_up scales"),
-            _dev(down[0], "down"), _dev(down[1], "down scales"),
-            _dev(sh_gate_up[0], "sh_gate_up"), _dev(sh_gate_up[1], "sh_gate_up scales"),
-            _dev(sh_down[0], "sh_down"), _dev(sh_down[1], "sh_down scales"),
-            _dev(topk_idx, "topk_idx"), _dev(topk_w, "topk_w"), N, D, E, d, d_sh, k, group,
-            inf if gate_max is None else float(gate_max), inf if up_max is None else float(up_max),
-            _dev(y, "y"), _dev(workspace, "workspace"),
-            workspace.numel() * workspace.element_size(), _stream_on(dev, stream)),
-            "moe_forward_quant")
+    _call("moe_forward_quant", dev, stream, x.data_ptr(), gate_up[0].data_ptr(),
+          gate_up[1].data_ptr(), down[0].data_ptr(), down[1].data_ptr(), sh_gate_up[0].data_ptr(),
+          sh_gate_up[1].data_ptr(), sh_down[0].data_ptr(), sh_down[1].data_ptr(),
+          topk_idx.data_ptr(), topk_w.data_ptr(), N, D, E, d, d_sh, k, group,
+          inf if gate_max is None else float(gate_max), inf if up_max is None else float(up_max),
+          y.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size())
     return y
