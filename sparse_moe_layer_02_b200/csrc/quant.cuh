@@ -739,6 +739,375 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<RG, MT, KW, NT, G>::BLOCKS)
     }
 }
 
+// ---------------------------------------------------------------------------
+// The product of one matrix with more than 16 tokens.  There the register kernel's MMA
+// time grows with the tokens (mma.sync m16n8k16, 8 cycles each), so tcgen05 takes over:
+// a tile is 128 weight rows x up to 96 tokens, one block per SM.
+//
+//   warp 0       TMA producer of the codes: 128 columns (8 KiB) a stage
+//   warp 6       TMA producer of the tokens: two swizzled boxes of 64 columns a stage
+//   warp 1       MMA issuer: M = 128 rows, N = the tokens in steps of 16, K = 16
+//   warps 2-5    codes to bf16 integers -8..7 (exact), thread = row, written to TMEM,
+//                where the MMA takes its A operand from: through shared memory they would
+//                cost eight times the codes' bytes in writes and reads, and its bandwidth
+//                was what bound the kernel then (1500 cycles a stage)
+//   warp 7       tells the MMA warp when a stage's accumulators have been read
+//   warps 8-15   sums: each group has a TMEM accumulator of its own (4 to 12 take turns);
+//                thread = row; sum += scale * group, in fp32 registers
+//
+// The weights are not rounded: integers times tokens are exact in the MMA's fp32 and the
+// scale is applied once per group outside.  A K = 16 MMA takes 45 cycles or more however
+// few the tokens (64 at 128), so a tile of 128 columns takes 400-500 cycles, about what
+// its codes take from memory (330).  A wait costs the issuing thread some 200 cycles more
+// while MMAs are in flight, so it has one a stage: the tokens' arrival counts on the
+// unpacked tile's barrier, and so does warp 7, which waits for the accumulators.
+// ---------------------------------------------------------------------------
+constexpr int QW_THREADS = 512;
+constexpr int QW_ROWS = 128, QW_TOK = 96, QW_COLS = 128;
+constexpr int QW_CST = 8, QW_AST = 4; // stages of codes; of tokens
+constexpr int QW_UST = 2;             // of unpacked weights: 64 TMEM columns each, from QW_UCOL on
+constexpr int QW_UCOL = 512 - QW_UST * QW_COLS / 2;
+constexpr int QW_MAXACC = 12; // TMEM accumulators in turn: QW_UCOL columns / tokens of a tile
+constexpr int QW_C_BYTES = QW_ROWS * QW_COLS / 2;     // 8 KiB of codes
+constexpr int QW_X_HALF = QW_TOK * 128;               // 64 columns of the tokens
+constexpr int QW_X_BYTES = 2 * QW_X_HALF;             // 32 KiB
+constexpr int QW_SMEM = 1024 + QW_CST * QW_C_BYTES + QW_AST * QW_X_BYTES + 768;
+static_assert(QW_SMEM <= 232448, "shared memory");
+constexpr int QW_UNPACK = 4, QW_SUMS = 8;             // warps
+
+// 32 lanes x 16 consecutive 32-bit columns.
+__device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t *r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+
+// The same shape written: lane t's values to TMEM lane t, 32 consecutive columns.
+__device__ __forceinline__ void tmem_st_32x32b_x32(uint32_t taddr, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+        "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]),
+        "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]),
+        "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// D (+)= A B with A in TMEM (lane = row, 16 bf16 in 8 columns), B by descriptor.
+__device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                             uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate));
+}
+
+struct QuantWideArgs {
+    const __nv_bfloat16 *s;
+    __nv_bfloat16 *y;
+    int N, M, K;
+    int tok;        // tokens of a tile (a multiple of 16)
+    int accs, ld;   // batches of TMEM accumulators; columns of one
+    int nb, tts;    // row tiles, token tiles
+    uint64_t wait_limit_ns;
+};
+
+// A word's eight codes as the bf16 integers -8..7 in order: 128 + code, less 136.
+__device__ __forceinline__ uint4 codes_bf16x8(uint32_t w) {
+    const uint32_t even = w & 0x0F0F0F0Fu, odd = (w >> 4) & 0x0F0F0F0Fu;
+    const uint32_t lo = __byte_perm(even, odd, 0x5140), hi = __byte_perm(even, odd, 0x7362);
+    const uint32_t k = 0x43434343u; // exponent of 128 as the upper bytes
+    uint32_t v[4] = {__byte_perm(lo, k, 0x4140), __byte_perm(lo, k, 0x4342), __byte_perm(hi, k, 0x4140),
+                     __byte_perm(hi, k, 0x4342)};
+    const __nv_bfloat162 off(__ushort_as_bfloat16(0x4308), __ushort_as_bfloat16(0x4308)); // 136
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 o = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&v[i]), off);
+        v[i] = *reinterpret_cast<const uint32_t *>(&o);
+    }
+    return make_uint4(v[0], v[1], v[2], v[3]);
+}
+
+// Maps: mC codes [M, K/2] bytes, box 64 x 128, swizzled; mX tokens [N, K], box 64 x
+// the tile's tokens, swizzled (large boxes: each TMA load costs its issuer 75-150 cycles).
+template <int G>
+__global__ void __launch_bounds__(QW_THREADS, 1)
+    quant_wide_kernel(const __grid_constant__ CUtensorMap mC, const __grid_constant__ CUtensorMap mX,
+                      const QuantWideArgs a) {
+    constexpr int GROUPS = QW_COLS / G;        // of a stage
+    constexpr int BATCH = GROUPS > 1 ? 2 : 1;  // groups handed over at a time
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    uint8_t *cbuf = smem;
+    uint8_t *xbuf = cbuf + QW_CST * QW_C_BYTES;
+    uint64_t *cfull = reinterpret_cast<uint64_t *>(xbuf + QW_AST * QW_X_BYTES);
+    uint64_t *cempty = cfull + QW_CST;
+    uint64_t *afull = cempty + QW_CST, *aempty = afull + QW_AST;
+    uint64_t *uempty = aempty + QW_AST, *dfull = uempty + QW_UST, *dempty = dfull + QW_MAXACC, *drain = dempty + QW_MAXACC;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    const int warp = warp_id(), lane = lane_id();
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < QW_CST; ++i) {
+            mbar_init(&cfull[i], 1);
+            mbar_init(&cempty[i], QW_UNPACK);
+        }
+        for (int i = 0; i < QW_AST; ++i) {
+            mbar_init(&afull[i], QW_UNPACK + 2); // unpacked weights, tokens, accumulators
+            mbar_init(&aempty[i], 1);
+        }
+        for (int i = 0; i < QW_UST; ++i) mbar_init(&uempty[i], 1);
+        for (int i = 0; i < QW_MAXACC; ++i) {
+            mbar_init(&dfull[i], 1);
+            mbar_init(&dempty[i], QW_SUMS);
+        }
+        mbar_init(drain, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+        tma_prefetch_desc(&mC);
+        tma_prefetch_desc(&mX);
+    }
+    // All that follows comes after the previous kernel of the stream.
+    grid_dep_wait();
+    grid_dep_launch_dependents();
+    if (warp == 1) {
+        tmem_alloc(tmem_slot, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+    const int total = a.nb * a.tts; // token tiles of one row tile are neighbours
+    const int stages = (a.K + QW_COLS - 1) / QW_COLS, groups = a.K / G;
+    const uint64_t limit = a.wait_limit_ns;
+
+    if (warp == 0 || warp == 6) {
+        if (lane == 0) {
+            const bool codes = warp == 0;
+            uint64_t *full = codes ? cfull : afull, *empty = codes ? cempty : aempty;
+            const uint32_t ring = codes ? QW_CST : QW_AST;
+            uint32_t it = 0, s = 0, ph = 0;
+            bool ok = true;
+            for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+                const int m0 = t / a.tts * QW_ROWS, n0 = t % a.tts * a.tok;
+                for (int i = 0; i < stages; ++i, ++it) {
+                    if (!mbar_wait(&empty[s], ph ^ 1, limit, abort_flag, codes ? 501 : 503)) { ok = false; break; }
+                    if (codes) {
+                        mbar_arrive_expect_tx(&full[s], QW_C_BYTES);
+                        tma_load_2d(&mC, &full[s], cbuf + s * QW_C_BYTES, i * (QW_COLS / 2), m0);
+                    } else {
+                        mbar_arrive_expect_tx(&full[s], a.tok * 256);
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+                            tma_load_2d(&mX, &full[s], xbuf + s * QW_X_BYTES + h * QW_X_HALF, i * QW_COLS + h * 64,
+                                        n0);
+                    }
+                    if (++s == ring) {
+                        s = 0;
+                        ph ^= 1;
+                    }
+                }
+            }
+            if (!ok) {
+                // Let copies already issued land before the CTA's memory goes away.
+                const uint32_t first = it > ring ? it - ring : 0;
+                for (uint32_t j = first; j < it; ++j) {
+                    volatile int no_abort = 0;
+                    mbar_wait(&full[j % ring], (j / ring) & 1, 10000000ull, &no_abort, 502);
+                }
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (lane == 0) {
+            uint32_t it = 0, d = 0; // stages so far; accumulators of a batch
+            bool ok = true;
+            for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+                const int n = (min(a.tok, a.N - t % a.tts * a.tok) + 15) & ~15;
+                const uint32_t idesc = umma_idesc_bf16(QW_ROWS, n);
+                for (int i = 0; i < stages && ok; ++i, ++it) {
+                    const uint32_t b = it % QW_AST;
+                    if (!mbar_wait(&afull[b], (it / QW_AST) & 1, limit, abort_flag, 512)) { ok = false; break; }
+                    tc_fence_after();
+                    const uint64_t dx = umma_desc_sw128(smem_u32(xbuf + b * QW_X_BYTES));
+                    const uint32_t ta = tmem_base + QW_UCOL + it % QW_UST * (QW_COLS / 2);
+                    for (int u = 0; u < GROUPS && i * GROUPS + u < groups; ++u) {
+#pragma unroll
+                        for (int kk = 0; kk < G / 16; ++kk) {
+                            const int k = u * (G / 16) + kk; // step of 16 columns in the stage
+                            // (8 columns of A; steps of the descriptor's address field)
+                            umma_bf16_ts(tmem_base + (d * BATCH + u % BATCH) * a.ld, ta + k * 8,
+                                         dx + ((k >> 2) * (QW_X_HALF / 16) + (k & 3) * 2), idesc, kk > 0 ? 1u : 0u);
+                        }
+                        if (u % BATCH == BATCH - 1 || i * GROUPS + u == groups - 1) {
+                            umma_commit(&dfull[d]);
+                            if (++d == (uint32_t)a.accs) d = 0;
+                        }
+                    }
+                    umma_commit(&uempty[it % QW_UST]);
+                    umma_commit(&aempty[b]);
+                }
+            }
+            // Drain: wait until every MMA issued by this thread has completed.
+            umma_commit(drain);
+            volatile int no_abort = 0;
+            mbar_wait(drain, 0, 100000000ull, &no_abort, 514);
+        }
+        __syncwarp();
+    } else if (warp < 2 + QW_UNPACK) {
+        // Row q * 32 + lane: its 64 bytes of codes are four pieces, swizzled by TMA.
+        const int q = warp & 3, row = q * 32 + lane;
+        const uint32_t ta = tmem_base + QW_UCOL + ((uint32_t)(q * 32) << 16);
+        uint32_t it = 0;
+        bool ok = true;
+        for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+            for (int i = 0; i < stages; ++i, ++it) {
+                const uint32_t s = it % QW_CST, b = it % QW_AST, u = it % QW_UST;
+                ok = mbar_wait(&cfull[s], (it / QW_CST) & 1, limit, abort_flag, 521);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                uint4 v[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    v[j] = *reinterpret_cast<const uint4 *>(cbuf + s * QW_C_BYTES + row * 64 +
+                                                            ((j ^ ((row >> 1) & 3)) << 4));
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&cempty[s]);
+                // the MMAs that read this part of TMEM, and the tokens' stage, are done
+                ok = mbar_wait(&uempty[u], ((it / QW_UST) & 1) ^ 1, limit, abort_flag, 522) &&
+                     mbar_wait(&aempty[b], ((it / QW_AST) & 1) ^ 1, limit, abort_flag, 523);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                tc_fence_after();
+#pragma unroll
+                for (int h = 0; h < 2; ++h) { // 64 columns each
+                    uint32_t o[32];
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const uint4 w = v[2 * h + j];
+                        const uint4 e[4] = {codes_bf16x8(w.x), codes_bf16x8(w.y), codes_bf16x8(w.z), codes_bf16x8(w.w)};
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            o[j * 16 + r * 4] = e[r].x;
+                            o[j * 16 + r * 4 + 1] = e[r].y;
+                            o[j * 16 + r * 4 + 2] = e[r].z;
+                            o[j * 16 + r * 4 + 3] = e[r].w;
+                        }
+                    }
+                    tmem_st_32x32b_x32(ta + u * (QW_COLS / 2) + h * 32, o);
+                }
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&afull[b]);
+            }
+        }
+    } else if (warp == 7) {
+        if (lane == 0) {
+            uint32_t it = 0, d = 0, ph = 0;
+            bool ok = true;
+            for (int t = blockIdx.x; t < total && ok; t += gridDim.x)
+                for (int i = 0; i < stages && ok; ++i, ++it) {
+                    const uint32_t b = it % QW_AST;
+                    ok = mbar_wait(&aempty[b], ((it / QW_AST) & 1) ^ 1, limit, abort_flag, 541);
+                    for (int u = 0; u < GROUPS && i * GROUPS + u < groups && ok; u += BATCH) {
+                        ok = mbar_wait(&dempty[d], ph ^ 1, limit, abort_flag, 542);
+                        if (++d == (uint32_t)a.accs) {
+                            d = 0;
+                            ph ^= 1;
+                        }
+                    }
+                    if (ok) mbar_arrive(&afull[b]);
+                }
+        }
+        __syncwarp();
+    } else if (warp >= 8) {
+        const int q = warp & 3; // TMEM lanes 32 q ..: rows q*32 + lane of the tile
+        // this warp's tokens of the tile: the first or the second half, in steps of 16
+        const int first = (warp >> 2) & 1 ? (a.tok / 2 + 15) & ~15 : 0;
+        const int most = (warp >> 2) & 1 ? QW_TOK : (a.tok / 2 + 15) & ~15;
+        uint32_t d = 0, ph = 0;
+        for (int t = blockIdx.x; t < total; t += gridDim.x) {
+            const int m = t / a.tts * QW_ROWS + q * 32 + lane, n0 = t % a.tts * a.tok;
+            const int cnt = min(min(a.tok, a.N - n0), most) - first; // tokens of this warp (any sign)
+            const __nv_bfloat16 *sp = a.s + min(m, a.M - 1);
+            float acc[48];
+#pragma unroll
+            for (int c = 0; c < 48; ++c) acc[c] = 0.f;
+            bool ok = true;
+            // Scales of four groups, and the next four on their way (some 1000 cycles from
+            // memory; moving a register waits for its load, so they move once in four).
+            __nv_bfloat16 sc[4], next[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) next[j] = sp[(size_t)min(j, groups - 1) * a.M];
+            for (int g0 = 0; g0 < groups; g0 += BATCH) {
+                if ((g0 & 3) == 0) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        sc[j] = next[j];
+                        next[j] = sp[(size_t)min(g0 + 4 + j, groups - 1) * a.M];
+                    }
+                }
+                ok = mbar_wait(&dfull[d], ph, limit, abort_flag, 531);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                tc_fence_after();
+#pragma unroll
+                for (int u = 0; u < BATCH; ++u) {
+                    const int gi = g0 + u;
+                    if (u && gi >= groups) break;
+                    const float s = __bfloat162float(gi & 2 ? (gi & 1 ? sc[3] : sc[2]) : (gi & 1 ? sc[1] : sc[0]));
+                    const uint32_t base = tmem_base + (d * BATCH + u) * a.ld + first + ((uint32_t)(q * 32) << 16);
+                    uint32_t v[48];
+#pragma unroll
+                    for (int c = 0; c < 3; ++c)
+                        if (cnt > c * 16) tmem_ld_32x32b_x16(base + c * 16, v + c * 16);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int c = 0; c < 3; ++c)
+                        if (cnt > c * 16) {
+#pragma unroll
+                            for (int j = 0; j < 16; ++j)
+                                acc[c * 16 + j] = fmaf(s, __uint_as_float(v[c * 16 + j]), acc[c * 16 + j]);
+                        }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&dempty[d]);
+                if (++d == (uint32_t)a.accs) {
+                    d = 0;
+                    ph ^= 1;
+                }
+            }
+            if (!ok) break;
+            if (m < a.M) {
+                __nv_bfloat16 *y = a.y + (size_t)(n0 + first) * a.M + m;
+#pragma unroll
+                for (int c = 0; c < 48; ++c)
+                    if (c < cnt) y[(size_t)c * a.M] = __float2bfloat16_rn(acc[c]);
+            }
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem_base, 512);
+    }
+}
+
 // y(n) = the k weighted expert rows in slot order + the shared expert's row, fp32,
 // rounded once.  One thread per 8 columns.
 __global__ void __launch_bounds__(128) quant_combine_kernel(const QuantArgs a, const float *slot,

@@ -111,6 +111,71 @@ int linear_quant_t(const void *q, const void *s, QuantArgs a, DeviceInfo *info, 
     return launch_quant<QUANT_LINEAR, RG, MT, KW, NT>(mW, mS, mW, mS, a, tiles, info, st);
 }
 
+template <int G>
+int launch_quant_wide(const CUtensorMap &mC, const CUtensorMap &mX, const QuantWideArgs &a, int grid,
+                      cudaStream_t st) {
+    static bool attr_set[kMaxDevices] = {}; // function attributes are set per device
+    const int dev = current_device_index();
+    if (dev < 0) return MOE_ERR_CUDA;
+    {
+        std::lock_guard<std::mutex> lk(g_mu);
+        if (!attr_set[dev]) {
+            if (cudaFuncSetAttribute(quant_wide_kernel<G>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     QW_SMEM) != cudaSuccess)
+                return MOE_ERR_CUDA;
+            attr_set[dev] = true;
+        }
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid, 1, 1);
+    cfg.blockDim = dim3(QW_THREADS, 1, 1);
+    cfg.dynamicSmemBytes = QW_SMEM;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (launch_ex(cfg, quant_wide_kernel<G>, mC, mX, a) != cudaSuccess) return MOE_ERR_CUDA;
+    return launch_status();
+}
+
+// y = x w^T for more than 16 tokens.
+int linear_quant_wide(const void *x, const void *q, const void *s, int N, int M, int K, int G, void *y,
+                      DeviceInfo *info, cudaStream_t st) {
+    QuantWideArgs a = {};
+    a.s = static_cast<const __nv_bfloat16 *>(s);
+    a.y = static_cast<__nv_bfloat16 *>(y);
+    a.N = N;
+    a.M = M;
+    a.K = K;
+    a.tts = (N + QW_TOK - 1) / QW_TOK;
+    a.tok = ((N + a.tts - 1) / a.tts + 15) / 16 * 16; // even tiles
+    a.tts = (N + a.tok - 1) / a.tok;
+    a.nb = (M + QW_ROWS - 1) / QW_ROWS;
+    a.ld = (a.tok + 31) / 32 * 32;
+    a.accs = std::min(QW_UCOL / a.ld, QW_MAXACC) / (G < QW_COLS ? 2 : 1);
+    a.wait_limit_ns = g_wait_limit_ns;
+    CUtensorMap mC, mX;
+    auto fn = encode_fn();
+    if (!fn) return MOE_ERR_CUDA;
+    cuuint64_t dims[2] = {(cuuint64_t)K / 2, (cuuint64_t)M};
+    cuuint64_t strides[1] = {(cuuint64_t)K / 2};
+    cuuint32_t box[2] = {QW_COLS / 2, QW_ROWS};
+    cuuint32_t estr[2] = {1, 1};
+    if (fn(&mC, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(q), dims, strides, box, estr,
+           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS ||
+        !make_map(&mX, x, K, N, K, a.tok))
+        return MOE_ERR_CUDA;
+    const int grid = (int)std::min<size_t>((size_t)a.nb * a.tts, (size_t)info->sms);
+    switch (G) {
+    case 32: return launch_quant_wide<32>(mC, mX, a, grid, st);
+    case 64: return launch_quant_wide<64>(mC, mX, a, grid, st);
+    default: return launch_quant_wide<128>(mC, mX, a, grid, st);
+    }
+}
+
 // ---- the layer ----
 struct QuantWs {
     size_t chunk_hist, counts, tile_off, meta, pos_of, perm_tok, w_perm, h, h_s, slot, osh, total;
@@ -269,7 +334,7 @@ int moe_linear_quant(const void *x, const void *q, const void *scales, int N, in
         return linear_quant_t<4, 2, 128, 1>(q, scales, a, dev, st);
     }
     if (N <= 16) return linear_quant_t<4, 2, 128, 2>(q, scales, a, dev, st);
-    return linear_quant_t<8, 2, 128, 4>(q, scales, a, dev, st);
+    return linear_quant_wide(x, q, scales, N, M, K, group, y, dev, st);
 }
 
 size_t moe_forward_quant_workspace(int N, int D, int E, int d_moe, int d_sh, int k) {
