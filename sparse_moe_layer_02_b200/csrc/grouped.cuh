@@ -14,7 +14,7 @@
 //
 // bf16: tcgen05.mma, 128 x 256 output tiles, k-blocks of 64, fp32 accumulators in
 // TMEM, one rounding to bf16.  Persistent, one CTA per SM, warp-specialised like the
-// forward's GEMMs: warp 0 TMA, warp 1 MMA, warps 2-5 epilogue; two accumulators.
+// forward's GEMMs: warp 0 TMA, warp 1 MMA, the others epilogue; two accumulators.
 // The operands keep their memory layout.  Where the summed index is contiguous the
 // shared-memory tile is K-major (forward both, dgrad dy); where it is the row the
 // tile is MN-major (dgrad W, wgrad both) and the MMA reads it transposed.
@@ -31,18 +31,26 @@ constexpr int GRP_BM = 128;
 constexpr int GRP_BN = 256;
 constexpr int GRP_BK = 64;
 constexpr int GRP_STAGES = 4;
-constexpr int GRP_THREADS = 192;
 constexpr int GRP_MAXE = 512;
 constexpr int GRP_A_BYTES = GRP_BM * GRP_BK * 2; // 16 KiB
 constexpr int GRP_B_BYTES = GRP_BN * GRP_BK * 2; // 32 KiB
 constexpr int GRP_STAGE_BYTES = GRP_A_BYTES + GRP_B_BYTES;
 constexpr int GRP_CHUNK = 64 * 64 * 2; // an MN-major box: 64 rows of 64 elements
-constexpr int GRP_OUT_BUF = 32 * 32 * 2;
-constexpr int GRP_TAB_OFF = GRP_STAGES * GRP_STAGE_BYTES + 256;
-constexpr int GRP_STG_OFF = (GRP_TAB_OFF + 2 * (GRP_MAXE + 1) * 4 + 1023) / 1024 * 1024;
-constexpr int GRP_SMEM_BYTES = 1024 + GRP_STG_OFF + 4 * 2 * GRP_OUT_BUF;
-static_assert(GRP_SMEM_BYTES <= 232448, "shared memory");
-static_assert((2 * GRP_STAGES + 5) * 8 + 8 <= 256, "barrier block");
+constexpr int GRP_OUT_BUF = 32 * 64 * 2; // an epilogue warp's store box: 32 rows of 64 elements
+// Shared memory (1024-byte aligned base): ring, one store box per epilogue warp, barriers,
+// segment tables.  wgrad's tiles are short (an expert's rows), so its epilogue counts: it
+// has eight warps instead of four; their boxes leave room for one table, all that it needs.
+template <int MODE> struct GrpCfg {
+    static constexpr int EPI = MODE == GRP_WGRAD ? 8 : 4; // epilogue warps
+    static constexpr int THREADS = 64 + 32 * EPI;
+    static constexpr int COLS = GRP_BN * 4 / EPI;         // of a tile, per warp
+    static constexpr int STG_OFF = GRP_STAGES * GRP_STAGE_BYTES;
+    static constexpr int BAR_OFF = STG_OFF + EPI * GRP_OUT_BUF;
+    static constexpr int TAB_OFF = BAR_OFF + 128;
+    static constexpr int SMEM = TAB_OFF + (MODE == GRP_WGRAD ? 1 : 2) * (GRP_MAXE + 1) * 4;
+    static_assert(SMEM <= 232448, "shared memory");
+};
+static_assert((2 * GRP_STAGES + 5) * 8 + 8 <= 128, "barrier block");
 
 struct GroupedArgs {
     const int32_t *offsets; // [E+1]
@@ -52,6 +60,7 @@ struct GroupedArgs {
     int ncols;    // output columns: forward M, dgrad K, wgrad K
     int nb;       // output column blocks
     int mb;       // wgrad: output row blocks
+    int wide;     // MN-major operands: one load for all of a tile's 64-column boxes
     void *out;
     int zero_rest; // forward, dgrad: write zeros to the rows of no expert
     uint64_t wait_limit_ns;
@@ -77,6 +86,14 @@ __device__ __forceinline__ void tma_load_3d(const CUtensorMap *map, uint64_t *ba
         "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
         : "memory");
 }
+__device__ __forceinline__ void tma_load_4d(const CUtensorMap *map, uint64_t *bar, void *dst,
+                                            int c0, int c1, int c2, int c3) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+        : "memory");
+}
 __device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, const void *src, int c0, int c1,
                                              int c2) {
     asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
@@ -86,8 +103,8 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, const void 
 }
 
 // The segment table: s_off[0..E] the offsets, made safe (within [0, rows] and not
-// decreasing; what was not is reported by one CTA), and s_tile[0..E] the prefix of
-// row tiles of `tile` rows.  One warp; lanes take consecutive experts.
+// decreasing; what was not is reported by one CTA), and s_tile[0..E] (unless null) the
+// prefix of row tiles of `tile` rows.  One warp; lanes take consecutive experts.
 __device__ __forceinline__ void grouped_table(const int32_t *offsets, int E, int rows, int tile,
                                               int *s_off, int *s_tile, bool report, int lane) {
     int top = 0; // running maximum of the offsets
@@ -109,6 +126,7 @@ __device__ __forceinline__ void grouped_table(const int32_t *offsets, int E, int
     }
     if (report && __any_sync(0xffffffffu, bad) && lane == 0) record_error(DEV_BAD_INDEX, 300);
     __syncwarp();
+    if (!s_tile) return;
     int carry = 0;
     for (int base = 0; base <= E; base += 32) {
         const int e = base + lane;
@@ -172,27 +190,29 @@ __device__ __forceinline__ GroupedTile grouped_tile(int t, const GroupedArgs &a,
     return c;
 }
 
-// Maps.  forward: mA x [rows, K] box 64 x 128 rows, mB W [E, M, K] box 64 x 256 x 1,
-// mOut y [rows, M] box 32 x 32.  dgrad: mA dy [rows, M] box 64 x 128, mB W box
+// Maps (wide, for columns that are a multiple of 64: an MN-major operand with its columns
+// in blocks of 64 as a dimension of their own, so that one load brings all of a tile's
+// boxes; a load costs its issuer 75-150 cycles, and six of them were more than a k-block's
+// MMAs).  forward: mA x [rows, K] box 64 x 128 rows, mB W [E, M, K] box 64 x 256 x 1,
+// mOut y [rows, M] box 64 x 32.  dgrad: mA dy [rows, M] box 64 x 128, mB W box
 // 64 x 64 x 1, mOut dx [rows, K].  wgrad: mA dy box 64 x 64, mB x [rows, K] box
-// 64 x 64, mOut dW [E, M, K] box 32 x 32 x 1.
+// 64 x 64, mOut dW [E, M, K] box 64 x 32 x 1.
 template <int MODE>
-__global__ void __launch_bounds__(GRP_THREADS, 1)
+__global__ void __launch_bounds__(GrpCfg<MODE>::THREADS, 1)
     grouped_product_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtensorMap mB,
                            const __grid_constant__ CUtensorMap mOut, const GroupedArgs a) {
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *smem = reinterpret_cast<uint8_t *>(
-        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    using C = GrpCfg<MODE>;
+    extern __shared__ __align__(1024) uint8_t smem[];
     uint8_t *ring = smem;
-    uint64_t *full = reinterpret_cast<uint64_t *>(smem + GRP_STAGES * GRP_STAGE_BYTES);
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::BAR_OFF);
     uint64_t *empty = full + GRP_STAGES;
     uint64_t *tfull = empty + GRP_STAGES;
     uint64_t *tempty = tfull + 2;
     uint64_t *drain = tempty + 2;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-    int *s_off = reinterpret_cast<int *>(smem + GRP_TAB_OFF);
-    int *s_tile = s_off + GRP_MAXE + 1;
+    int *s_off = reinterpret_cast<int *>(smem + C::TAB_OFF);
+    int *s_tile = MODE == GRP_WGRAD ? nullptr : s_off + GRP_MAXE + 1;
 
     const int warp = warp_id(), lane = lane_id();
     if (threadIdx.x == 0) {
@@ -202,7 +222,7 @@ __global__ void __launch_bounds__(GRP_THREADS, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&tfull[i], 1);
-            mbar_init(&tempty[i], 4);
+            mbar_init(&tempty[i], C::EPI);
         }
         mbar_init(drain, 1);
         *abort_flag = 0;
@@ -247,9 +267,16 @@ __global__ void __launch_bounds__(GRP_THREADS, 1)
                         tma_load_3d(&mB, &full[s], sb, kx, c.n0, c.e);
                     } else if (MODE == GRP_DGRAD) {
                         tma_load_2d(&mA, &full[s], sa, kx, c.r0);
+                        if (a.wide) {
+                            tma_load_4d(&mB, &full[s], sb, 0, kx, c.n0 / 64, c.e);
+                        } else {
 #pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            tma_load_3d(&mB, &full[s], sb + j * GRP_CHUNK, c.n0 + 64 * j, kx, c.e);
+                            for (int j = 0; j < 4; ++j)
+                                tma_load_3d(&mB, &full[s], sb + j * GRP_CHUNK, c.n0 + 64 * j, kx, c.e);
+                        }
+                    } else if (a.wide) {
+                        tma_load_3d(&mA, &full[s], sa, 0, c.r0 + kx, c.m0 / 64);
+                        tma_load_3d(&mB, &full[s], sb, 0, c.r0 + kx, c.n0 / 64);
                     } else {
 #pragma unroll
                         for (int j = 0; j < 2; ++j)
@@ -341,8 +368,9 @@ __global__ void __launch_bounds__(GRP_THREADS, 1)
     } else {
         // ------------------------------ epilogue ---------------------------------
         const int q = warp & 3; // TMEM lane quadrant: output rows q*32 + lane of the tile
-        uint8_t *stg = smem + GRP_STG_OFF + q * 2 * GRP_OUT_BUF;
-        uint32_t nstore = 0, tc = 0;
+        const int part = (warp - 2) >> 2; // of the tile's columns
+        uint8_t *stg = smem + C::STG_OFF + (warp - 2) * GRP_OUT_BUF + lane * 128; // this lane's row
+        uint32_t tc = 0;
         for (int t = blockIdx.x; t < total; t += gridDim.x) {
             const GroupedTile c = grouped_tile<MODE>(t, a, s_off, s_tile);
             const bool none = c.kb == 0; // nothing accumulated: zeros
@@ -357,66 +385,68 @@ __global__ void __launch_bounds__(GRP_THREADS, 1)
             if (!have) continue;
             tc_fence_after();
             const uint32_t tbase = tmem_base + acc * GRP_BN + ((uint32_t)(q * 32) << 16);
-            // Rows of this warp: wgrad's past M are clipped by the store's map; in the
-            // other modes a part of 32 rows inside the segment is stored by TMA, a
-            // ragged one by each row's thread.
-            const int first = q * 32;
-            const int rows = MODE == GRP_WGRAD ? a.M - c.m0 - first : c.r1 - c.r0 - first;
+            const int first = q * 32; // this warp's rows of the tile
+            const int rows = (MODE == GRP_WGRAD ? a.M - c.m0 : c.r1 - c.r0) - first;
+            if (none) {
+                // zeros: one row after the other, whole lines at a time
+                const int cols = min(GRP_BN, a.ncols - c.n0) / 8;
+                for (int r = part; r < min(32, rows); r += C::EPI / 4)
+                    if (lane < cols)
+                        reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) +
+                                                  ((size_t)c.e * a.M + c.m0 + first + r) * a.ncols + c.n0)[lane] =
+                            make_uint4(0u, 0u, 0u, 0u);
+                continue;
+            }
+            // wgrad's rows past M are clipped by the store's map; in the other modes a part
+            // of 32 rows inside the segment is stored by TMA, a ragged one by each row's
+            // thread.  64 columns at a time: while one box is read from shared memory, the
+            // next columns come from TMEM (boxes of 32 columns, two in turn: 1300 cycles
+            // each, more than the MMAs of a short tile).
             const bool by_tma = MODE == GRP_WGRAD || rows >= 32;
 #pragma unroll 1
-            for (int ch = 0; ch < GRP_BN / 32; ++ch) {
-                const int col = c.n0 + ch * 32;
+            for (int ch = part * C::COLS / 64; ch < (part + 1) * C::COLS / 64; ++ch) {
+                const int col = c.n0 + ch * 64;
                 if (col >= a.ncols || rows <= 0) break;
-                uint32_t v[32];
-                if (none) {
+                uint32_t v[2][32];
+                tmem_ld_32x32b_x32(tbase + ch * 64, v[0]);
+                tmem_ld_32x32b_x32(tbase + ch * 64 + 32, v[1]);
+                tmem_ld_wait();
+                uint4 u[8];
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] = 0u;
-                } else {
-                    tmem_ld_32x32b_x32(tbase + ch * 32, v);
-                    tmem_ld_wait();
+                for (int j = 0; j < 8; ++j) {
+                    const uint32_t *f = &v[j / 4][(j % 4) * 8];
+                    u[j] = make_uint4(pack_bf16x2(__uint_as_float(f[0]), __uint_as_float(f[1])),
+                                      pack_bf16x2(__uint_as_float(f[2]), __uint_as_float(f[3])),
+                                      pack_bf16x2(__uint_as_float(f[4]), __uint_as_float(f[5])),
+                                      pack_bf16x2(__uint_as_float(f[6]), __uint_as_float(f[7])));
                 }
-                uint32_t pk[16];
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    pk[i] = pack_bf16x2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
-                const uint4 u[4] = {make_uint4(pk[0], pk[1], pk[2], pk[3]),
-                                    make_uint4(pk[4], pk[5], pk[6], pk[7]),
-                                    make_uint4(pk[8], pk[9], pk[10], pk[11]),
-                                    make_uint4(pk[12], pk[13], pk[14], pk[15])};
                 if (by_tma) {
-                    uint8_t *buf = stg + (nstore & 1) * GRP_OUT_BUF;
-                    if (lane == 0) bulk_wait_group_read<1>(); // the box staged 2 ago left buf
+                    if (lane == 0) bulk_wait_group_read<0>(); // the last box has left the buffer
                     __syncwarp();
-                    uint4 *dst = reinterpret_cast<uint4 *>(buf + lane * 64);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int p = (j + lane) & 3; // fewer bank conflicts
-                        dst[p] = p == 0 ? u[0] : p == 1 ? u[1] : p == 2 ? u[2] : u[3];
-                    }
+                    for (int j = 0; j < 8; ++j) // at the places of the 128-byte swizzle
+                        *reinterpret_cast<uint4 *>(stg + ((j ^ (lane & 7)) << 4)) = u[j];
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) {
                         if (MODE == GRP_WGRAD)
-                            tma_store_3d(&mOut, buf, col, c.m0 + first, c.e);
+                            tma_store_3d(&mOut, stg, col, c.m0 + first, c.e);
                         else
-                            tma_store_2d(&mOut, buf, col, c.r0 + first);
+                            tma_store_2d(&mOut, stg, col, c.r0 + first);
                         bulk_commit_group();
                     }
-                    ++nstore;
                 } else if (lane < rows) {
                     uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) +
                                                            (size_t)(c.r0 + first + lane) * a.ncols + col);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
+                    for (int j = 0; j < 8; ++j)
                         if (col + 8 * j < a.ncols) dst[j] = u[j];
                 }
             }
-            if (!none) {
-                // Release the accumulator.
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&tempty[acc]);
-            }
+            // Release the accumulator.
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&tempty[acc]);
         }
         if (lane == 0) bulk_wait_group<0>(); // stores done
         if (MODE != GRP_WGRAD && a.zero_rest)

@@ -7,10 +7,10 @@
 namespace moe {
 namespace {
 
-// 3-D bf16 map over [d2, d1, d0] (d0 contiguous), boxes of b0 x b1 x 1 elements;
-// out-of-range elements read as zero and are not written.
+// 3-D bf16 map over [d2, d1, d0] (d0 contiguous), boxes of b0 x b1 x 1 elements with
+// 128-byte swizzle; out-of-range elements read as zero and are not written.
 bool make_map3(CUtensorMap *m, const void *base, uint64_t d0, uint64_t d1, uint64_t d2, uint32_t b0,
-               uint32_t b1, bool swizzle) {
+               uint32_t b1) {
     auto fn = encode_fn();
     if (!fn) return false;
     cuuint64_t dims[3] = {d0, d1, d2};
@@ -19,9 +19,23 @@ bool make_map3(CUtensorMap *m, const void *base, uint64_t d0, uint64_t d1, uint6
     cuuint32_t estr[3] = {1, 1, 1};
     return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box,
               estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
-              swizzle ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B : CU_TENSOR_MAP_L2_PROMOTION_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The same with the columns in blocks of 64: [d2, cols / 64, d1, 64], boxes of blocks x
+// rows x 64 elements.  cols is a multiple of 64.
+bool make_map_blocks(CUtensorMap *m, const void *base, uint64_t cols, uint64_t d1, uint64_t d2,
+                     uint32_t rows, uint32_t blocks, bool batched) {
+    auto fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[4] = {64, d1, cols / 64, d2};
+    cuuint64_t strides[3] = {cols * 2, 128, cols * d1 * 2};
+    cuuint32_t box[4] = {64, rows, blocks, 1};
+    cuuint32_t estr[4] = {1, 1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, batched ? 4 : 3, const_cast<void *>(base), dims, strides,
+              box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int MODE>
@@ -35,12 +49,12 @@ int launch_grouped(const CUtensorMap &mA, const CUtensorMap &mB, const CUtensorM
         if (!attr_set[dev]) {
             if (cudaFuncSetAttribute(grouped_product_kernel<MODE>,
                                      cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     GRP_SMEM_BYTES) != cudaSuccess)
+                                     GrpCfg<MODE>::SMEM) != cudaSuccess)
                 return MOE_ERR_CUDA;
             attr_set[dev] = true;
         }
     }
-    grouped_product_kernel<MODE><<<grid, GRP_THREADS, GRP_SMEM_BYTES, st>>>(mA, mB, mOut, a);
+    grouped_product_kernel<MODE><<<grid, GrpCfg<MODE>::THREADS, GrpCfg<MODE>::SMEM, st>>>(mA, mB, mOut, a);
     return launch_status();
 }
 
@@ -107,14 +121,19 @@ int grouped_impl(const void *A, const void *B, const int32_t *offsets, int rows,
     CUtensorMap mA, mB, mOut;
     bool ok;
     if (MODE == GRP_FORWARD)
-        ok = make_map(&mA, A, K, rows, K, GRP_BM) && make_map3(&mB, B, K, M, E, 64, GRP_BN, true) &&
-             make_map_out(&mOut, out, M, rows, M);
-    else if (MODE == GRP_DGRAD)
-        ok = make_map(&mA, A, M, rows, M, GRP_BM) && make_map3(&mB, B, K, M, E, 64, 64, true) &&
-             make_map_out(&mOut, out, K, rows, K);
-    else
-        ok = make_map(&mA, A, M, rows, M, 64) && make_map(&mB, B, K, rows, K, 64) &&
-             make_map3(&mOut, out, K, M, E, 32, 32, false);
+        ok = make_map(&mA, A, K, rows, K, GRP_BM) && make_map3(&mB, B, K, M, E, 64, GRP_BN) &&
+             make_map(&mOut, out, M, rows, M, 32);
+    else if (MODE == GRP_DGRAD) {
+        a.wide = K % 64 == 0;
+        ok = make_map(&mA, A, M, rows, M, GRP_BM) && make_map(&mOut, out, K, rows, K, 32) &&
+             (a.wide ? make_map_blocks(&mB, B, K, M, E, 64, 4, true) : make_map3(&mB, B, K, M, E, 64, 64));
+    } else {
+        a.wide = K % 64 == 0 && M % 64 == 0;
+        ok = make_map3(&mOut, out, K, M, E, 64, 32) &&
+             (a.wide ? make_map_blocks(&mA, A, M, rows, 1, 64, 2, false) &&
+                           make_map_blocks(&mB, B, K, rows, 1, 64, 4, false)
+                     : make_map(&mA, A, M, rows, M, 64) && make_map(&mB, B, K, rows, K, 64));
+    }
     if (!ok) return MOE_ERR_CUDA;
     const size_t tiles = MODE == GRP_WGRAD ? (size_t)E * a.nb * a.mb
                                            : ((size_t)rows / GRP_BM + std::min(rows, E)) * a.nb;
