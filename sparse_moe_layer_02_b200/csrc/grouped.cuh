@@ -463,16 +463,50 @@ __global__ void __launch_bounds__(GrpCfg<MODE>::THREADS, 1)
 }
 
 // ---------------------------------------------------------------------------
-// fp32: the same three products on the CUDA cores, T x T output tiles, 16 summed
+// fp32: the same three products on the CUDA cores, T x T output tiles, 32 summed
 // indices at a time in shared memory, 4 x 4 sums a thread (fp32, one running sum in
-// index order).  The summed index never crosses a segment, so nothing is masked but
-// loads.  T = 64 for large batches, 32 for small ones (more tiles for the same SMs).
+// index order); the next 32 are on their way from memory meanwhile.  The summed index
+// never crosses a segment, so nothing is masked but loads.  T = 64 for large batches, 32
+// for small ones (more tiles for the same SMs).
 // ---------------------------------------------------------------------------
+// Element (k, i) of an operand in shared memory; loads are 16 bytes along the contiguous
+// index: the summed one (KCONT) or the other.
+template <bool KCONT, int T, int NT> struct F32Operand {
+    static constexpr int KB = 32, PER = KB * T / 4 / NT; // pieces of a thread
+    float4 v[PER];
+    // rows: of the contiguous direction's other index; ld: elements from one to the next
+    __device__ __forceinline__ void load(const float *p, size_t ld, int nk, int ni, int tid) {
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+            const int at = tid + j * NT;
+            const int k = KCONT ? at % (KB / 4) * 4 : at / (T / 4), i = KCONT ? at / (KB / 4) : at % (T / 4) * 4;
+            v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (k < nk && i < ni) // counts along the contiguous index are multiples of 4
+                v[j] = *reinterpret_cast<const float4 *>(p + (KCONT ? (size_t)i * ld + k : (size_t)k * ld + i));
+        }
+    }
+    __device__ __forceinline__ void store(float (*s)[T + 4], int tid) const {
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+            const int at = tid + j * NT;
+            if (KCONT) {
+                const int k = at % (KB / 4) * 4, i = at / (KB / 4);
+                s[k][i] = v[j].x;
+                s[k + 1][i] = v[j].y;
+                s[k + 2][i] = v[j].z;
+                s[k + 3][i] = v[j].w;
+            } else {
+                *reinterpret_cast<float4 *>(&s[at / (T / 4)][at % (T / 4) * 4]) = v[j];
+            }
+        }
+    }
+};
+
 template <int MODE, int T>
 __global__ void __launch_bounds__((T / 4) * (T / 4)) grouped_f32_kernel(const float *A, const float *B,
                                                                         const GroupedArgs a) {
-    constexpr int NT = (T / 4) * (T / 4), KB = 16;
-    __shared__ float sA[KB][T + 4], sB[KB][T + 4];
+    constexpr int NT = (T / 4) * (T / 4), KB = 32;
+    __shared__ __align__(16) float sA[KB][T + 4], sB[KB][T + 4];
     __shared__ int s_off[GRP_MAXE + 1], s_tile[GRP_MAXE + 1];
     const int tid = threadIdx.x;
     if (tid < 32) grouped_table(a.offsets, a.E, a.rows, T, s_off, s_tile, blockIdx.x == 0, tid);
@@ -501,31 +535,28 @@ __global__ void __launch_bounds__((T / 4) * (T / 4)) grouped_f32_kernel(const fl
             red = a.red;
         }
         const float *We = B + (size_t)e * a.M * a.K; // forward, dgrad
+        F32Operand<MODE != GRP_WGRAD, T, NT> fa;     // forward x[i][k], dgrad dy[i][k], wgrad dy[r0+k][i]
+        F32Operand<MODE == GRP_FORWARD, T, NT> fb;   // forward W[n][k], dgrad W[k][n], wgrad x[r0+k][n]
+        auto fetch = [&](int k0) {
+            if (MODE == GRP_WGRAD) {
+                fa.load(A + (size_t)(r0 + k0) * a.M + i0, a.M, red - k0, i1 - i0, tid);
+                fb.load(B + (size_t)(r0 + k0) * a.K + n0, a.K, red - k0, a.ncols - n0, tid);
+            } else {
+                fa.load(A + (size_t)i0 * a.red + k0, a.red, red - k0, i1 - i0, tid);
+                if (MODE == GRP_FORWARD)
+                    fb.load(We + (size_t)n0 * a.K + k0, a.K, red - k0, a.ncols - n0, tid);
+                else
+                    fb.load(We + (size_t)k0 * a.K + n0, a.K, red - k0, a.ncols - n0, tid);
+            }
+        };
         float acc[4][4] = {};
+        if (red > 0) fetch(0);
         for (int k0 = 0; k0 < red; k0 += KB) {
-            for (int j = tid; j < KB * T; j += NT) {
-                // A(i, k): forward x[i][k], dgrad dy[i][k]: k contiguous; wgrad dy[r0+k][i]
-                const int k = MODE == GRP_WGRAD ? j / T : j % KB;
-                const int i = MODE == GRP_WGRAD ? j % T : j / KB;
-                float v = 0.f;
-                if (k0 + k < red && i0 + i < i1)
-                    v = MODE == GRP_WGRAD ? A[(size_t)(r0 + k0 + k) * a.M + i0 + i]
-                                          : A[(size_t)(i0 + i) * a.red + k0 + k];
-                sA[k][i] = v;
-            }
-            for (int j = tid; j < KB * T; j += NT) {
-                // B(k, n): forward W[n][k]; dgrad W[k][n]; wgrad x[r0+k][n]
-                const int k = MODE == GRP_FORWARD ? j % KB : j / T;
-                const int n = MODE == GRP_FORWARD ? j / KB : j % T;
-                float v = 0.f;
-                if (k0 + k < red && n0 + n < a.ncols)
-                    v = MODE == GRP_FORWARD ? We[(size_t)(n0 + n) * a.K + k0 + k]
-                        : MODE == GRP_DGRAD ? We[(size_t)(k0 + k) * a.K + n0 + n]
-                                            : B[(size_t)(r0 + k0 + k) * a.K + n0 + n];
-                sB[k][n] = v;
-            }
+            fa.store(sA, tid);
+            fb.store(sB, tid);
             __syncthreads();
-#pragma unroll
+            if (k0 + KB < red) fetch(k0 + KB);
+#pragma unroll 8
             for (int k = 0; k < KB; ++k) {
                 const float4 x = *reinterpret_cast<const float4 *>(&sA[k][ty * 4]);
                 const float4 w = *reinterpret_cast<const float4 *>(&sB[k][tx * 4]);

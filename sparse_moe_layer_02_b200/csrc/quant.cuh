@@ -23,43 +23,48 @@ namespace moe {
 // bytes + 2/G per weight either way; a warp keeps 4 rows (64 bytes a lane) in flight to
 // quantize and 8 rows (32 bytes a lane) to dequantize.
 //
-// w / s is taken as w * (1/s), rounded to a multiple of 2^-12 on the way (one
-// multiply-add with 1.5 * 2^11).  That gives round(w / s) exactly: w and s have 8-bit
-// significands, so a quotient between 1/4 and 8 either is a multiple of 1/2 or lies at
-// least 2^-11 away from every odd multiple of 1/2, while the product is within 2^-19 of
-// the quotient.  |w / s| < 7.5 for scales that are normal numbers; below 2^-120, where s
-// or 1/s is not, the code comes from the division and is clamped.
+// Both quotients are products with a reciprocal, and exact all the same.  max|w| / 7 is
+// never nearer than 1/14 of a step to a tie of its rounding to bf16 (an 8-bit integer is
+// no odd multiple of 7/2), the product within 2^-22 of it.  w / s is rounded to a multiple
+// of 2^-12 on the way (the multiply-add with 1.5 * 2^11), then to an integer, half to
+// even: w and s have 8-bit significands, so a quotient between 1/4 and 8 either is a
+// multiple of 1/2 or lies at least 2^-11 away from every odd multiple of 1/2, while the
+// product is within 2^-19 of the quotient.  |w / s| < 7.5 for scales that are normal
+// numbers; below 2^-120, where s or 1/s is not, the code comes from the division and is
+// clamped.  (With divisions and a mask and shift for each code the issue slots bound the
+// kernel: 640 us for 32 x 4096 x 6144, 3.2 TB/s.)
 // ---------------------------------------------------------------------------
 constexpr int QZ_ROWS = 32, DQ_ROWS = 64, QZ_COLS = 256, QZ_THREADS = 256;
 
+template <int G>
 __global__ void __launch_bounds__(QZ_THREADS) quantize_kernel(const __nv_bfloat16 *__restrict__ W,
                                                               uint8_t *__restrict__ q,
-                                                              __nv_bfloat16 *__restrict__ s, int M, int K,
-                                                              int G) {
+                                                              __nv_bfloat16 *__restrict__ s, int M, int K) {
     constexpr int RW = QZ_ROWS / 8; // rows of a warp
     __shared__ __nv_bfloat16 ss[QZ_COLS / 32][QZ_ROWS];
     const int lane = lane_id(), warp = warp_id();
     const int k = blockIdx.x * QZ_COLS + lane * 8, m0 = blockIdx.y * QZ_ROWS;
     const size_t e = blockIdx.z;
-    const int per = G >> 3; // lanes of a group
+    constexpr int PER = G / 8; // lanes of a group
+    const int rows = k < K ? min(RW, M - m0 - warp * RW) : 0; // of this lane
+    const size_t at = (e * M + m0 + warp * RW) * (size_t)K + k;
     uint4 v[RW];
 #pragma unroll
     for (int i = 0; i < RW; ++i) {
-        const int m = m0 + warp * RW + i;
         v[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (m < M && k < K)
-            v[i] = __ldcs(reinterpret_cast<const uint4 *>(W + (e * M + m) * (size_t)K + k));
+        if (i < rows) v[i] = __ldcs(reinterpret_cast<const uint4 *>(W + at + (size_t)i * K));
     }
+    uint8_t *qp = q + at / 2;
 #pragma unroll
     for (int i = 0; i < RW; ++i) {
-        const int m = m0 + warp * RW + i;
         // The largest magnitude, two columns at a time (a NaN wins over all).
         const __nv_bfloat162 *b = reinterpret_cast<const __nv_bfloat162 *>(&v[i]);
         __nv_bfloat162 t2 = __hmax2_nan(__hmax2_nan(__habs2(b[0]), __habs2(b[1])),
                                         __hmax2_nan(__habs2(b[2]), __habs2(b[3])));
-        for (int d = 1; d < per; d <<= 1) t2 = __hmax2_nan(t2, __shfl_xor_sync(0xffffffffu, t2, d));
+#pragma unroll
+        for (int d = 1; d < PER; d <<= 1) t2 = __hmax2_nan(t2, __shfl_xor_sync(0xffffffffu, t2, d));
         const float top = __bfloat162float(__hmax_nan(__low2bfloat16(t2), __high2bfloat16(t2)));
-        __nv_bfloat16 sb = __float2bfloat16_rn(top / 7.0f);
+        __nv_bfloat16 sb = __float2bfloat16_rn(top * (1.0f / 7.0f));
         if (!(top < INFINITY)) sb = __ushort_as_bfloat16(0x7FFF); // every value NaN
         const float sf = __bfloat162float(sb);
         float w[8];
@@ -69,12 +74,13 @@ __global__ void __launch_bounds__(QZ_THREADS) quantize_kernel(const __nv_bfloat1
         unpack_bf16x2(v[i].w, w[6], w[7]);
         uint32_t c = 0;
         if (sf >= 0x1p-120f) {
-            const float r = 1.0f / sf;
+            float r;
+            asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(sf));
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float t = fmaf(w[j], r, 3072.0f) - 3072.0f;    // a multiple of 2^-12
-                const uint32_t n = __float_as_uint(t + 12582920.0f); // 1.5 * 2^23 + 8: code in the low bits
-                c |= (n & 15u) << (4 * j);
+            for (int j = 7; j >= 0; --j) {
+                const float u = fmaf(w[j], r, 3072.0f);                      // 3072 + a multiple of 2^-12
+                const uint32_t n = __float_as_uint(u + (12582920.0f - 3072.0f)); // 0x4B400000 + code
+                c = c * 16u + (n - 0x4B400000u);
             }
         } else {
 #pragma unroll
@@ -84,34 +90,50 @@ __global__ void __launch_bounds__(QZ_THREADS) quantize_kernel(const __nv_bfloat1
                 c |= (uint32_t)((int)t + 8) << (4 * j);
             }
         }
-        if (m < M && k < K) *reinterpret_cast<uint32_t *>(q + (e * M + m) * (size_t)(K / 2) + k / 2) = c;
-        if ((lane & (per - 1)) == 0) ss[lane / per][warp * RW + i] = sb;
+        if (i < rows) *reinterpret_cast<uint32_t *>(qp + (size_t)i * (K / 2)) = c;
+        if (lane % PER == 0) ss[lane / PER][warp * RW + i] = sb;
     }
     __syncthreads();
-    const int groups = QZ_COLS / G;
+    constexpr int groups = QZ_COLS / G;
     const int g = threadIdx.x / QZ_ROWS, r = threadIdx.x % QZ_ROWS; // 8 groups at most
     const int kg = blockIdx.x * groups + g;
     if (g < groups && kg < K / G && m0 + r < M) s[(e * (K / G) + kg) * (size_t)M + m0 + r] = ss[g][r];
 }
 
+// A word's eight codes as the bf16 integers -8..7 in order: 128 + code, less 136.
+__device__ __forceinline__ uint4 codes_bf16x8(uint32_t w) {
+    const uint32_t even = w & 0x0F0F0F0Fu, odd = (w >> 4) & 0x0F0F0F0Fu;
+    const uint32_t lo = __byte_perm(even, odd, 0x5140), hi = __byte_perm(even, odd, 0x7362);
+    const uint32_t k = 0x43434343u; // exponent of 128 as the upper bytes
+    uint32_t v[4] = {__byte_perm(lo, k, 0x4140), __byte_perm(lo, k, 0x4342), __byte_perm(hi, k, 0x4140),
+                     __byte_perm(hi, k, 0x4342)};
+    const __nv_bfloat162 off(__ushort_as_bfloat16(0x4308), __ushort_as_bfloat16(0x4308)); // 136
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 o = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&v[i]), off);
+        v[i] = *reinterpret_cast<const uint32_t *>(&o);
+    }
+    return make_uint4(v[0], v[1], v[2], v[3]);
+}
+
+template <int G>
 __global__ void __launch_bounds__(QZ_THREADS) dequantize_kernel(const uint8_t *__restrict__ q,
                                                                 const __nv_bfloat16 *__restrict__ s,
-                                                                __nv_bfloat16 *__restrict__ W, int M, int K,
-                                                                int G) {
+                                                                __nv_bfloat16 *__restrict__ W, int M, int K) {
     constexpr int RW = DQ_ROWS / 8;
     __shared__ __nv_bfloat16 ss[QZ_COLS / 32][DQ_ROWS];
     const int lane = lane_id(), warp = warp_id();
     const int k = blockIdx.x * QZ_COLS + lane * 8, m0 = blockIdx.y * DQ_ROWS;
     const size_t e = blockIdx.z;
+    const int rows = k < K ? min(RW, M - m0 - warp * RW) : 0; // of this lane
+    const size_t at = (e * M + m0 + warp * RW) * (size_t)K + k;
     uint32_t c[RW];
 #pragma unroll
     for (int i = 0; i < RW; ++i) {
-        const int m = m0 + warp * RW + i;
         c[i] = 0;
-        if (m < M && k < K)
-            c[i] = __ldcs(reinterpret_cast<const uint32_t *>(q + (e * M + m) * (size_t)(K / 2) + k / 2));
+        if (i < rows) c[i] = __ldcs(reinterpret_cast<const uint32_t *>(q + (at / 2 + (size_t)i * (K / 2))));
     }
-    const int groups = QZ_COLS / G;
+    constexpr int groups = QZ_COLS / G;
     for (int j = threadIdx.x; j < groups * DQ_ROWS; j += QZ_THREADS) {
         const int g = j / DQ_ROWS, r = j % DQ_ROWS, kg = blockIdx.x * groups + g;
         if (kg < K / G && m0 + r < M) ss[g][r] = s[(e * (K / G) + kg) * (size_t)M + m0 + r];
@@ -119,15 +141,17 @@ __global__ void __launch_bounds__(QZ_THREADS) dequantize_kernel(const uint8_t *_
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < RW; ++i) {
-        const int m = m0 + warp * RW + i;
-        if (m >= M || k >= K) continue;
-        const float sf = __bfloat162float(ss[lane * 8 / G][warp * RW + i]);
-        uint32_t o[4];
+        if (i >= rows) break;
+        // integers -8..7 times the scale, in bf16: the one rounding
+        const __nv_bfloat162 sb = __bfloat162bfloat162(ss[lane * 8 / G][warp * RW + i]);
+        uint4 v = codes_bf16x8(c[i]);
+        uint32_t o[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) // products of 4 and 8 bits are exact in fp32
-            o[j] = pack_bf16x2((float)((int)((c[i] >> (8 * j)) & 15u) - 8) * sf,
-                               (float)((int)((c[i] >> (8 * j + 4)) & 15u) - 8) * sf);
-        __stcs(reinterpret_cast<uint4 *>(W + (e * M + m) * (size_t)K + k), make_uint4(o[0], o[1], o[2], o[3]));
+        for (int j = 0; j < 4; ++j) {
+            const __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&o[j]), sb);
+            o[j] = *reinterpret_cast<const uint32_t *>(&r);
+        }
+        __stcs(reinterpret_cast<uint4 *>(W + at + (size_t)i * K), make_uint4(o[0], o[1], o[2], o[3]));
     }
 }
 
@@ -819,22 +843,6 @@ struct QuantWideArgs {
     int nb, tts;    // row tiles, token tiles
     uint64_t wait_limit_ns;
 };
-
-// A word's eight codes as the bf16 integers -8..7 in order: 128 + code, less 136.
-__device__ __forceinline__ uint4 codes_bf16x8(uint32_t w) {
-    const uint32_t even = w & 0x0F0F0F0Fu, odd = (w >> 4) & 0x0F0F0F0Fu;
-    const uint32_t lo = __byte_perm(even, odd, 0x5140), hi = __byte_perm(even, odd, 0x7362);
-    const uint32_t k = 0x43434343u; // exponent of 128 as the upper bytes
-    uint32_t v[4] = {__byte_perm(lo, k, 0x4140), __byte_perm(lo, k, 0x4342), __byte_perm(hi, k, 0x4140),
-                     __byte_perm(hi, k, 0x4342)};
-    const __nv_bfloat162 off(__ushort_as_bfloat16(0x4308), __ushort_as_bfloat16(0x4308)); // 136
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const __nv_bfloat162 o = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&v[i]), off);
-        v[i] = *reinterpret_cast<const uint32_t *>(&o);
-    }
-    return make_uint4(v[0], v[1], v[2], v[3]);
-}
 
 // Maps: mC codes [M, K/2] bytes, box 64 x 128, swizzled; mX tokens [N, K], box 64 x
 // the tile's tokens, swizzled (large boxes: each TMA load costs its issuer 75-150 cycles).

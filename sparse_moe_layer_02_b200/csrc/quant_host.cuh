@@ -288,9 +288,16 @@ int moe_quantize(const void *W, int E, int M, int K, int group, void *q, void *s
     if (rc != MOE_OK) return rc;
     if (dev->major != 10) return MOE_ERR_NO_DEVICE;
     const dim3 grid((K + QZ_COLS - 1) / QZ_COLS, (M + QZ_ROWS - 1) / QZ_ROWS, E);
-    quantize_kernel<<<grid, QZ_THREADS, 0, static_cast<cudaStream_t>(stream)>>>(
-        static_cast<const __nv_bfloat16 *>(W), static_cast<uint8_t *>(q), static_cast<__nv_bfloat16 *>(scales),
-        M, K, group);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const auto *w = static_cast<const __nv_bfloat16 *>(W);
+    auto *c = static_cast<uint8_t *>(q);
+    auto *s = static_cast<__nv_bfloat16 *>(scales);
+    if (group == 32)
+        quantize_kernel<32><<<grid, QZ_THREADS, 0, st>>>(w, c, s, M, K);
+    else if (group == 64)
+        quantize_kernel<64><<<grid, QZ_THREADS, 0, st>>>(w, c, s, M, K);
+    else
+        quantize_kernel<128><<<grid, QZ_THREADS, 0, st>>>(w, c, s, M, K);
     return launch_status();
 }
 
@@ -303,9 +310,16 @@ int moe_dequantize(const void *q, const void *scales, int E, int M, int K, int g
     if (rc != MOE_OK) return rc;
     if (dev->major != 10) return MOE_ERR_NO_DEVICE;
     const dim3 grid((K + QZ_COLS - 1) / QZ_COLS, (M + DQ_ROWS - 1) / DQ_ROWS, E);
-    dequantize_kernel<<<grid, QZ_THREADS, 0, static_cast<cudaStream_t>(stream)>>>(
-        static_cast<const uint8_t *>(q), static_cast<const __nv_bfloat16 *>(scales),
-        static_cast<__nv_bfloat16 *>(W), M, K, group);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const auto *c = static_cast<const uint8_t *>(q);
+    const auto *s = static_cast<const __nv_bfloat16 *>(scales);
+    auto *w = static_cast<__nv_bfloat16 *>(W);
+    if (group == 32)
+        dequantize_kernel<32><<<grid, QZ_THREADS, 0, st>>>(c, s, w, M, K);
+    else if (group == 64)
+        dequantize_kernel<64><<<grid, QZ_THREADS, 0, st>>>(c, s, w, M, K);
+    else
+        dequantize_kernel<128><<<grid, QZ_THREADS, 0, st>>>(c, s, w, M, K);
     return launch_status();
 }
 
