@@ -231,6 +231,10 @@ __global__ void __launch_bounds__(GrpCfg<MODE>::THREADS, 1)
         tma_prefetch_desc(&mB);
         tma_prefetch_desc(&mOut);
     }
+    // Nothing above touches global memory; all that follows comes after the previous
+    // kernel of the stream.
+    grid_dep_wait();
+    grid_dep_launch_dependents();
     if (warp == 1) {
         tmem_alloc(tmem_slot, 512);
         tmem_relinquish();
@@ -509,6 +513,8 @@ __global__ void __launch_bounds__((T / 4) * (T / 4)) grouped_f32_kernel(const fl
     __shared__ __align__(16) float sA[KB][T + 4], sB[KB][T + 4];
     __shared__ int s_off[GRP_MAXE + 1], s_tile[GRP_MAXE + 1];
     const int tid = threadIdx.x;
+    grid_dep_wait(); // all that follows comes after the previous kernel of the stream
+    grid_dep_launch_dependents();
     if (tid < 32) grouped_table(a.offsets, a.E, a.rows, T, s_off, s_tile, blockIdx.x == 0, tid);
     __syncthreads();
     const int total = MODE == GRP_WGRAD ? a.E * a.nb * a.mb : s_tile[a.E] * a.nb;

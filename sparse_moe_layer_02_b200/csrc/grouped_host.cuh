@@ -38,6 +38,24 @@ bool make_map_blocks(CUtensorMap *m, const void *base, uint64_t cols, uint64_t d
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// A launch with programmatic stream serialization: the kernel may become resident while
+// its predecessor ends, and waits for it (griddepcontrol.wait) before it touches memory.
+template <typename... KArgs, typename... Args>
+int launch_serial(void (*kernel)(KArgs...), dim3 grid, int threads, int smem, cudaStream_t st, Args &&...args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (launch_ex(cfg, kernel, args...) != cudaSuccess) return MOE_ERR_CUDA;
+    return launch_status();
+}
+
 template <int MODE>
 int launch_grouped(const CUtensorMap &mA, const CUtensorMap &mB, const CUtensorMap &mOut,
                    const GroupedArgs &a, int grid, cudaStream_t st) {
@@ -54,8 +72,8 @@ int launch_grouped(const CUtensorMap &mA, const CUtensorMap &mB, const CUtensorM
             attr_set[dev] = true;
         }
     }
-    grouped_product_kernel<MODE><<<grid, GrpCfg<MODE>::THREADS, GrpCfg<MODE>::SMEM, st>>>(mA, mB, mOut, a);
-    return launch_status();
+    return launch_serial(grouped_product_kernel<MODE>, dim3(grid, 1, 1), GrpCfg<MODE>::THREADS,
+                         GrpCfg<MODE>::SMEM, st, mA, mB, mOut, a);
 }
 
 // One product.  A and B: forward x, W; dgrad dy, W; wgrad dy, x.
@@ -109,11 +127,8 @@ int grouped_impl(const void *A, const void *B, const int32_t *offsets, int rows,
                                                : ((size_t)rows / T + std::min(rows, E)) * a.nb;
         const int grid = (int)std::min<size_t>(std::max<size_t>(tiles, 1), (size_t)dev->sms * 8);
         const float *fa = static_cast<const float *>(A), *fb = static_cast<const float *>(B);
-        if (small)
-            grouped_f32_kernel<MODE, 32><<<grid, 64, 0, st>>>(fa, fb, a);
-        else
-            grouped_f32_kernel<MODE, 64><<<grid, 256, 0, st>>>(fa, fb, a);
-        return launch_status();
+        if (small) return launch_serial(grouped_f32_kernel<MODE, 32>, dim3(grid, 1, 1), 64, 0, st, fa, fb, a);
+        return launch_serial(grouped_f32_kernel<MODE, 64>, dim3(grid, 1, 1), 256, 0, st, fa, fb, a);
     }
 
     a.nb = (a.ncols + GRP_BN - 1) / GRP_BN;

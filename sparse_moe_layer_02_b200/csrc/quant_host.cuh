@@ -126,18 +126,7 @@ int launch_quant_wide(const CUtensorMap &mC, const CUtensorMap &mX, const QuantW
             attr_set[dev] = true;
         }
     }
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid, 1, 1);
-    cfg.blockDim = dim3(QW_THREADS, 1, 1);
-    cfg.dynamicSmemBytes = QW_SMEM;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (launch_ex(cfg, quant_wide_kernel<G>, mC, mX, a) != cudaSuccess) return MOE_ERR_CUDA;
-    return launch_status();
+    return launch_serial(quant_wide_kernel<G>, dim3(grid, 1, 1), QW_THREADS, QW_SMEM, st, mC, mX, a);
 }
 
 // y = x w^T for more than 16 tokens.
@@ -437,19 +426,11 @@ int moe_forward_quant(const void *x, const void *gate_up, const void *gate_up_sc
          : W.tile_rows == 16 ? quant_layer_t<8, 2, 128, 2>(w, a, x, ws, W, dev, prof, st)
                              : quant_layer_t<8, 2, 128, 4>(w, a, x, ws, W, dev, prof, st);
     if (rc != MOE_OK) return rc;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(N, (D + 1023) / 1024, 1);
-    cfg.blockDim = dim3(128, 1, 1);
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (launch_ex(cfg, quant_combine_kernel, a, (const float *)(ws + W.slot), (const float *)(ws + W.osh),
-                  (const int32_t *)dp.pos_of, static_cast<__nv_bfloat16 *>(y), D) != cudaSuccess)
-        return MOE_ERR_CUDA;
-    return launched(prof);
+    rc = launch_serial(quant_combine_kernel, dim3(N, (D + 1023) / 1024, 1), 128, 0, st, a,
+                       (const float *)(ws + W.slot), (const float *)(ws + W.osh), (const int32_t *)dp.pos_of,
+                       static_cast<__nv_bfloat16 *>(y), D);
+    prof.mark();
+    return rc;
 }
 
 }  // extern "C"
