@@ -97,9 +97,9 @@ def _linear(x, W, offsets, y, stream):
 
 class _GroupedLinear(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, W, offsets, stream):
+    def forward(ctx, x, W, offsets):
         ctx.save_for_backward(x, W, offsets)
-        return _linear(x, W, offsets, None, stream)
+        return _linear(x, W, offsets, None, None)
 
     @staticmethod
     @torch.autograd.function.once_differentiable
@@ -108,7 +108,33 @@ class _GroupedLinear(torch.autograd.Function):
         dy = dy.contiguous()
         dx = moe_grouped_linear_dgrad(dy, W, offsets) if ctx.needs_input_grad[0] else None
         dW = moe_grouped_linear_wgrad(dy, x, offsets) if ctx.needs_input_grad[1] else None
-        return dx, dW, None, None
+        return dx, dW, None
+
+
+def _accumulation(leaf):
+    """The notes (a dict) of the node that accumulates a leaf's gradient."""
+    return torch.autograd.graph.get_gradient_edge(leaf).node.metadata
+
+
+def _differentiable(x, W, offsets):
+    """_GroupedLinear, refusing a capture on a leaf whose gradient accumulation belongs to an
+    eager pass.
+
+    Autograd keeps one accumulation node per leaf while any pass holds it, tied to the stream
+    it was made on.  A backward pass captured on another stream would have to join that
+    stream, which ends the capture and the process.  So every call leaves its stream on the
+    nodes (which its own pass now holds), and a captured one reads it first."""
+    leaves = [t for t in (x, W) if t.requires_grad and t.is_leaf]
+    here = torch.cuda.current_stream().cuda_stream
+    if torch.cuda.is_current_stream_capturing():
+        for t in leaves:
+            if _accumulation(t).get("moe_stream", here) != here:
+                raise ValueError("capturing: an eager pass over the same leaf tensors, made on another "
+                                 "stream, is still alive; drop its outputs first")
+    y = _GroupedLinear.apply(x, W, offsets)
+    for t in leaves:
+        _accumulation(t).setdefault("moe_stream", here)
+    return y
 
 
 def moe_grouped_linear(x, W, offsets, y=None, stream=None):
@@ -116,12 +142,13 @@ def moe_grouped_linear(x, W, offsets, y=None, stream=None):
 
     x [rows, K] and W [E, M, K] bf16 or fp32, offsets int32 [E + 1], all contiguous on one
     device.  A y that is given keeps its rows of no expert; a new one has zeros there.
-    Differentiable in x and W when no y and no stream is given (the backward pass runs on
-    the stream autograd gives it; rows of no expert have a zero gradient)."""
-    if y is None and torch.is_grad_enabled() and (x.requires_grad or W.requires_grad):
-        if stream is not None:
-            raise ValueError("stream: not with gradients (use torch.cuda.stream)")
-        return _GroupedLinear.apply(x, W, offsets, None)
+    Differentiable in x and W (rows of no expert have a zero gradient), without a y or a
+    stream of the caller's; the backward pass runs on the stream autograd gives it."""
+    if torch.is_grad_enabled() and (x.requires_grad or W.requires_grad):
+        if y is not None or stream is not None:
+            raise ValueError("y and stream: not with gradients (use torch.no_grad, torch.cuda.stream)")
+        with torch.cuda.device(_device(x, W, offsets)):
+            return _differentiable(x, W, offsets)
     return _linear(x, W, offsets, y, stream)
 
 

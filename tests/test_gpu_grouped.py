@@ -227,3 +227,114 @@ def test_refusals():
             bad()
     with pytest.raises(moe.MoEError):  # rows of 16 bytes
         moe.moe_grouped_linear(x[:, :20].contiguous(), W[:, :, :20].contiguous(), off)
+
+
+def test_capture_over_a_living_eager_pass_is_refused():
+    """Autograd would end the process in the captured backward; the captured forward raises."""
+    x, W, dy, off = _case([9, 30], 64, 48, BF16)
+    x.requires_grad_(True)
+    W.requires_grad_(True)
+    alive = moe.moe_grouped_linear(x, W, off)
+    g = torch.cuda.CUDAGraph()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with pytest.raises(ValueError, match="eager"):
+        with torch.cuda.graph(g, stream=s):
+            moe.moe_grouped_linear(x, W, off)
+    torch.cuda.synchronize()
+    alive.backward(dy)
+    want = x.grad.clone(), W.grad.clone()
+    del alive, g
+    # with the eager pass gone, forward and backward are captured and replayed
+    x.grad = W.grad = None
+    with torch.cuda.stream(s):
+        for _ in range(2):
+            gx, gW = torch.autograd.grad(moe.moe_grouped_linear(x, W, off), [x, W], dy)
+    del gx, gW
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        gx, gW = torch.autograd.grad(moe.moe_grouped_linear(x, W, off), [x, W], dy)
+    for t in (gx, gW):
+        t.fill_(float("nan"))
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(gx, want[0]) and torch.equal(gW, want[1])
+
+
+def test_an_output_with_gradients_is_refused():
+    x, W, dy, off = _case([9, 30], 64, 48, BF16)
+    W.requires_grad_(True)
+    with pytest.raises(ValueError):
+        moe.moe_grouped_linear(x, W, off, y=torch.empty_like(dy))
+    with torch.no_grad():
+        y = moe.moe_grouped_linear(x, W, off, y=torch.empty_like(dy))
+    assert torch.equal(y, moe.moe_grouped_linear(x, W.detach(), off))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_offsets_past_32_bits(dtype):
+    """More than 2^31 elements of x, and of W: the last rows and the last expert are right."""
+    K, M, rows = 4096, 8, 2 ** 31 // 4096 + 700
+    g = torch.Generator(device=DEV)
+    g.manual_seed(0)
+    x = torch.zeros((rows, K), dtype=dtype, device=DEV)
+    x[-500:] = torch.randn((500, K), generator=g, device=DEV).to(dtype)
+    W = torch.randn((2, M, K), generator=g, device=DEV).to(dtype)
+    dy = torch.ones((rows, M), dtype=dtype, device=DEV)
+    off = torch.tensor([0, rows - 333, rows], dtype=torch.int32, device=DEV)
+    xs, small = x[-500:].clone(), torch.tensor([0, 167, 500], dtype=torch.int32, device=DEV)
+    y = moe.moe_grouped_linear(x, W, off)
+    assert torch.equal(y[-500:], moe.moe_grouped_linear(xs, W, small))
+    assert (y[:-500] == 0).all()
+    del y
+    dx = moe.moe_grouped_linear_dgrad(dy, W, off)
+    assert torch.equal(dx[-500:], moe.moe_grouped_linear_dgrad(dy[-500:], W, small))
+    del dx
+    dW = moe.moe_grouped_linear_wgrad(dy, x, off)
+    assert torch.equal(dW[1], moe.moe_grouped_linear_wgrad(dy[-500:], xs, small)[1])
+    del x, W, dy, dW
+    E = 2 ** 31 // (1056 * 4096) + 1  # 497, of at most 512
+    W = torch.zeros((E, 1056, 4096), dtype=dtype, device=DEV)
+    W[-1] = torch.randn((1056, 4096), generator=g, device=DEV).to(dtype)
+    off = torch.zeros(E + 1, dtype=torch.int32, device=DEV)
+    off[-1] = 500
+    one = torch.tensor([0, 500], dtype=torch.int32, device=DEV)
+    assert torch.equal(moe.moe_grouped_linear(xs, W, off), moe.moe_grouped_linear(xs, W[-1:], one))
+    dy = torch.randn((500, 1056), generator=g, device=DEV).to(dtype)
+    assert torch.equal(moe.moe_grouped_linear_dgrad(dy, W, off), moe.moe_grouped_linear_dgrad(dy, W[-1:], one))
+    dW = moe.moe_grouped_linear_wgrad(dy, xs, off, dW=W)
+    assert torch.equal(dW[-1], moe.moe_grouped_linear_wgrad(dy, xs, one)[0]) and (dW[:-1] == 0).all()
+    assert moe.moe_device_status() == 0
+
+
+def test_a_wait_that_runs_out_is_reported_and_leaves_the_device_usable():
+    x, W, dy, off = _case([700, 300], 1024, 2048, BF16)
+    calls = (lambda: moe.moe_grouped_linear(x, W, off), lambda: moe.moe_grouped_linear_dgrad(dy, W, off),
+             lambda: moe.moe_grouped_linear_wgrad(dy, x, off))
+    want = [f() for f in calls]
+    assert moe.moe_device_status() == 0
+    try:
+        moe.moe_debug_set_wait_limit_ns(1)
+        for f in calls:
+            f()
+            assert moe.moe_device_status() in (0, -6)
+    finally:
+        moe.moe_debug_set_wait_limit_ns(0)
+    assert all(torch.equal(f(), w) for f, w in zip(calls, want))
+    assert moe.moe_device_status() == 0
+
+
+def test_two_streams_at_once():
+    a, b = _case([200, 3, 130], 264, 520, BF16), _case([64] * 9, 512, 256, BF16, seed=1)
+    want = [moe.moe_grouped_linear(c[0], c[1], c[3]) for c in (a, b)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for i, c in enumerate((a, b)):
+            got[i].append(moe.moe_grouped_linear(c[0], c[1], c[3], stream=streams[i],
+                                                 y=torch.empty_like(want[i])))
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, want[i]) for i in range(2) for y in got[i])
+    assert moe.moe_device_status() == 0

@@ -339,3 +339,74 @@ def test_refusals():
         _run(x, w, ids, tw, gate_max=float("nan"))
     assert moe.moe_linear_quant(x[:0], *w["sh_gate_up"]).shape == (0, 256)
     assert _run(x[:0], w, ids[:0], tw[:0]).shape == (0, 256)
+
+
+@pytest.mark.parametrize("N", [1, 5, 20, 97])
+def test_a_wait_that_runs_out_is_reported_and_leaves_the_device_usable(N):
+    g = _gen(N)
+    q, s = moe.moe_quantize(_randn(g, 1024, 4096, std=0.02), 64)
+    xl = _randn(g, N, 4096)
+    x, w, ids, tw = _layer(N, 512, 6, 2, 512, 256, 64)
+    calls = lambda: (moe.moe_linear_quant(xl, q, s), _run(x, w, ids, tw))
+    want = calls()
+    assert moe.moe_device_status() == 0
+    try:
+        moe.moe_debug_set_wait_limit_ns(1)
+        for _ in range(3):
+            calls()
+            assert moe.moe_device_status() in (0, -6)
+    finally:
+        moe.moe_debug_set_wait_limit_ns(0)
+    for a, b in zip(calls(), want):
+        assert torch.equal(a, b)
+    assert moe.moe_device_status() == 0
+
+
+def test_offsets_past_32_bits():
+    """More than 2^31 weights: the last matrix is converted like one by itself."""
+    E = 2 ** 31 // (1024 * 4096) + 1
+    W = torch.zeros((E, 1024, 4096), dtype=BF16, device=DEV)
+    W[-1] = _randn(_gen(0), 1024, 4096, std=0.02)
+    q, s = moe.moe_quantize(W, 128)
+    q1, s1 = moe.moe_quantize(W[-1], 128)
+    assert torch.equal(q[-1], q1) and torch.equal(s[-1], s1)
+    assert (q[:-1] == 0x88).all() and (s[:-1] == 0).all()
+    back = moe.moe_dequantize(q, s, W=W)
+    assert torch.equal(back[-1], moe.moe_dequantize(q1, s1)) and (back[:-1] == 0).all()
+
+
+@pytest.mark.parametrize("N,M,K,G", [(96, 128, 128, 128), (97, 136, 256, 32), (192, 264, 640, 64),
+                                     (193, 40, 384, 128), (300, 1000, 96, 32), (24, 4104, 64, 64)])
+def test_product_with_many_tokens(N, M, K, G):
+    g = _gen(N + M)
+    q, s = moe.moe_quantize(_randn(g, M, K, std=0.02), G)
+    x = _randn(g, N, K)
+    w = _values(q, s)
+    y = x.double() @ w.t()
+    bad = ~((moe.moe_linear_quant(x, q, s).double() - y).abs() <= _product_tol(x, w, K, y))
+    assert not bad.any(), (int(bad.sum()), bad.nonzero()[:4].tolist())
+    assert moe.moe_device_status() == 0
+
+
+def test_large_tokens():
+    """Tokens up to 2^62 and scales up to 2^50 are finite numbers like others."""
+    g = _gen(3)
+    q, s = moe.moe_quantize(_randn(g, 64, 256), 64)
+    x = _randn(g, 4, 256)
+    want = moe.moe_linear_quant(x, q, s)
+    assert torch.equal(moe.moe_linear_quant(x * 2.0 ** 60, q, s), want * 2.0 ** 60)
+    assert torch.equal(moe.moe_linear_quant(x * 2.0 ** -60, q, s), want * 2.0 ** -60)
+    assert torch.equal(moe.moe_linear_quant(x, q, s * 2.0 ** 50), want * 2.0 ** 50)
+
+
+def test_two_streams_at_once():
+    g = _gen(12)
+    ws = [moe.moe_quantize(_randn(g, 512, 1024, std=0.02), 64), moe.moe_quantize(_randn(g, 2048, 256, std=0.02), 32)]
+    xs = [_randn(g, 40, 1024), _randn(g, 3, 256)]
+    want = [moe.moe_linear_quant(x, *w) for x, w in zip(xs, ws)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = [[moe.moe_linear_quant(xs[i], *ws[i], y=torch.empty_like(want[i]), stream=streams[i])
+            for i in range(2)] for _ in range(20)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(y[i], want[i]) for y in got for i in range(2))
