@@ -769,24 +769,25 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<RG, MT, KW, NT, G>::BLOCKS)
 // a tile is 128 weight rows x up to 96 tokens, one block per SM.
 //
 //   warp 0       TMA producer of the codes: 128 columns (8 KiB) a stage
-//   warp 6       TMA producer of the tokens: two swizzled boxes of 64 columns a stage
-//   warp 1       MMA issuer: M = 128 rows, N = the tokens in steps of 16, K = 16
-//   warps 2-5    codes to bf16 integers -8..7 (exact), thread = row, written to TMEM,
+//   warp 2       TMA producer of the tokens: two swizzled boxes of 64 columns a stage
+//   warps 1, 3   MMA issuers, the stages in turn (every group has an accumulator of its
+//                own): M = 128 rows, N = the tokens in steps of 16, K = 16
+//   warps 4-11   codes to bf16 integers -8..7 (exact), thread = row, written to TMEM,
 //                where the MMA takes its A operand from: through shared memory they would
 //                cost eight times the codes' bytes in writes and reads, and its bandwidth
-//                was what bound the kernel then (1500 cycles a stage)
-//   warp 7       tells the MMA warp when a stage's accumulators have been read
-//   warps 8-15   sums: each group has a TMEM accumulator of its own (4 to 12 take turns);
+//                was what bound the kernel then (1500 cycles a stage); two teams of four
+//                warps take the stages in turn
+//   warps 12-19  sums: each group has a TMEM accumulator of its own (4 to 12 take turns);
 //                thread = row; sum += scale * group, in fp32 registers
 //
 // The weights are not rounded: integers times tokens are exact in the MMA's fp32 and the
 // scale is applied once per group outside.  A K = 16 MMA takes 45 cycles or more however
 // few the tokens (64 at 128), so a tile of 128 columns takes 400-500 cycles, about what
 // its codes take from memory (330).  A wait costs the issuing thread some 200 cycles more
-// while MMAs are in flight, so it has one a stage: the tokens' arrival counts on the
-// unpacked tile's barrier, and so does warp 7, which waits for the accumulators.
+// while MMAs are in flight, so there
+// are two issuers, and the tokens' arrival counts on the unpacked tile's barrier.
 // ---------------------------------------------------------------------------
-constexpr int QW_THREADS = 512;
+constexpr int QW_THREADS = 640;
 constexpr int QW_ROWS = 128, QW_TOK = 96, QW_COLS = 128;
 constexpr int QW_CST = 8, QW_AST = 4; // stages of codes; of tokens
 constexpr int QW_UST = 2;             // of unpacked weights: 64 TMEM columns each, from QW_UCOL on
@@ -861,7 +862,7 @@ __global__ void __launch_bounds__(QW_THREADS, 1)
     uint64_t *cempty = cfull + QW_CST;
     uint64_t *afull = cempty + QW_CST, *aempty = afull + QW_AST;
     uint64_t *uempty = aempty + QW_AST, *dfull = uempty + QW_UST, *dempty = dfull + QW_MAXACC, *drain = dempty + QW_MAXACC;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 2);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     const int warp = warp_id(), lane = lane_id();
 
@@ -871,7 +872,7 @@ __global__ void __launch_bounds__(QW_THREADS, 1)
             mbar_init(&cempty[i], QW_UNPACK);
         }
         for (int i = 0; i < QW_AST; ++i) {
-            mbar_init(&afull[i], QW_UNPACK + 2); // unpacked weights, tokens, accumulators
+            mbar_init(&afull[i], QW_UNPACK + 1); // unpacked weights, tokens
             mbar_init(&aempty[i], 1);
         }
         for (int i = 0; i < QW_UST; ++i) mbar_init(&uempty[i], 1);
@@ -879,7 +880,7 @@ __global__ void __launch_bounds__(QW_THREADS, 1)
             mbar_init(&dfull[i], 1);
             mbar_init(&dempty[i], QW_SUMS);
         }
-        mbar_init(drain, 1);
+        for (int i = 0; i < 2; ++i) mbar_init(&drain[i], 1);
         *abort_flag = 0;
         fence_mbar_init();
         tma_prefetch_desc(&mC);
@@ -900,7 +901,7 @@ __global__ void __launch_bounds__(QW_THREADS, 1)
     const int stages = (a.K + QW_COLS - 1) / QW_COLS, groups = a.K / G;
     const uint64_t limit = a.wait_limit_ns;
 
-    if (warp == 0 || warp == 6) {
+    if (warp == 0 || warp == 2) {
         if (lane == 0) {
             const bool codes = warp == 0;
             uint64_t *full = codes ? cfull : afull, *empty = codes ? cempty : aempty;
@@ -937,50 +938,73 @@ __global__ void __launch_bounds__(QW_THREADS, 1)
             }
         }
         __syncwarp();
-    } else if (warp == 1) {
+    } else if (warp == 1 || warp == 3) {
         if (lane == 0) {
-            uint32_t it = 0, d = 0; // stages so far; accumulators of a batch
+            const uint32_t turn = warp >> 1;
+            uint32_t it = 0, d = 0, ph = 0; // stages so far; accumulators of a batch and their round
             bool ok = true;
+            auto next = [&]() {
+                if (++d == (uint32_t)a.accs) {
+                    d = 0;
+                    ph ^= 1;
+                }
+            };
             for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
                 const int n = (min(a.tok, a.N - t % a.tts * a.tok) + 15) & ~15;
                 const uint32_t idesc = umma_idesc_bf16(QW_ROWS, n);
                 for (int i = 0; i < stages && ok; ++i, ++it) {
+                    const int ng = min(GROUPS, groups - i * GROUPS);
+                    if ((it & 1) != turn) {
+                        // The other's stage.  A wait must not fall two rounds behind its
+                        // barrier: with two batches a stage, this one waits here too.
+                        for (int u = 0; u < ng && ok; u += BATCH) {
+                            if (GROUPS > BATCH) ok = mbar_wait(&dempty[d], ph ^ 1, limit, abort_flag, 513);
+                            next();
+                        }
+                        continue;
+                    }
                     const uint32_t b = it % QW_AST;
                     if (!mbar_wait(&afull[b], (it / QW_AST) & 1, limit, abort_flag, 512)) { ok = false; break; }
-                    tc_fence_after();
                     const uint64_t dx = umma_desc_sw128(smem_u32(xbuf + b * QW_X_BYTES));
                     const uint32_t ta = tmem_base + QW_UCOL + it % QW_UST * (QW_COLS / 2);
-                    for (int u = 0; u < GROUPS && i * GROUPS + u < groups; ++u) {
+                    for (int u0 = 0; u0 < ng; u0 += BATCH) {
+                        if (!mbar_wait(&dempty[d], ph ^ 1, limit, abort_flag, 514)) { ok = false; break; }
+                        tc_fence_after();
 #pragma unroll
-                        for (int kk = 0; kk < G / 16; ++kk) {
-                            const int k = u * (G / 16) + kk; // step of 16 columns in the stage
-                            // (8 columns of A; steps of the descriptor's address field)
-                            umma_bf16_ts(tmem_base + (d * BATCH + u % BATCH) * a.ld, ta + k * 8,
-                                         dx + ((k >> 2) * (QW_X_HALF / 16) + (k & 3) * 2), idesc, kk > 0 ? 1u : 0u);
+                        for (int v = 0; v < BATCH; ++v) {
+                            const int u = u0 + v;
+                            if (u >= ng) break;
+#pragma unroll
+                            for (int kk = 0; kk < G / 16; ++kk) {
+                                const int k = u * (G / 16) + kk; // step of 16 columns in the stage
+                                // (8 columns of A; steps of the descriptor's address field)
+                                umma_bf16_ts(tmem_base + (d * BATCH + v) * a.ld, ta + k * 8,
+                                             dx + ((k >> 2) * (QW_X_HALF / 16) + (k & 3) * 2), idesc, kk > 0 ? 1u : 0u);
+                            }
                         }
-                        if (u % BATCH == BATCH - 1 || i * GROUPS + u == groups - 1) {
-                            umma_commit(&dfull[d]);
-                            if (++d == (uint32_t)a.accs) d = 0;
-                        }
+                        umma_commit(&dfull[d]);
+                        next();
                     }
+                    if (!ok) break;
                     umma_commit(&uempty[it % QW_UST]);
                     umma_commit(&aempty[b]);
                 }
             }
             // Drain: wait until every MMA issued by this thread has completed.
-            umma_commit(drain);
+            umma_commit(&drain[turn]);
             volatile int no_abort = 0;
-            mbar_wait(drain, 0, 100000000ull, &no_abort, 514);
+            mbar_wait(&drain[turn], 0, 100000000ull, &no_abort, 515);
         }
         __syncwarp();
-    } else if (warp < 2 + QW_UNPACK) {
+    } else if (warp >= 4 && warp < 12) {
         // Row q * 32 + lane: its 64 bytes of codes are four pieces, swizzled by TMA.
-        const int q = warp & 3, row = q * 32 + lane;
+        const int team = (warp - 4) >> 2, q = warp & 3, row = q * 32 + lane;
         const uint32_t ta = tmem_base + QW_UCOL + ((uint32_t)(q * 32) << 16);
         uint32_t it = 0;
         bool ok = true;
         for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
             for (int i = 0; i < stages; ++i, ++it) {
+                if ((int)(it & 1) != team) continue;
                 const uint32_t s = it % QW_CST, b = it % QW_AST, u = it % QW_UST;
                 ok = mbar_wait(&cfull[s], (it / QW_CST) & 1, limit, abort_flag, 521);
                 ok = __all_sync(0xffffffffu, ok);
@@ -1021,30 +1045,11 @@ __global__ void __launch_bounds__(QW_THREADS, 1)
                 if (lane == 0) mbar_arrive(&afull[b]);
             }
         }
-    } else if (warp == 7) {
-        if (lane == 0) {
-            uint32_t it = 0, d = 0, ph = 0;
-            bool ok = true;
-            for (int t = blockIdx.x; t < total && ok; t += gridDim.x)
-                for (int i = 0; i < stages && ok; ++i, ++it) {
-                    const uint32_t b = it % QW_AST;
-                    ok = mbar_wait(&aempty[b], ((it / QW_AST) & 1) ^ 1, limit, abort_flag, 541);
-                    for (int u = 0; u < GROUPS && i * GROUPS + u < groups && ok; u += BATCH) {
-                        ok = mbar_wait(&dempty[d], ph ^ 1, limit, abort_flag, 542);
-                        if (++d == (uint32_t)a.accs) {
-                            d = 0;
-                            ph ^= 1;
-                        }
-                    }
-                    if (ok) mbar_arrive(&afull[b]);
-                }
-        }
-        __syncwarp();
-    } else if (warp >= 8) {
+    } else {
         const int q = warp & 3; // TMEM lanes 32 q ..: rows q*32 + lane of the tile
         // this warp's tokens of the tile: the first or the second half, in steps of 16
-        const int first = (warp >> 2) & 1 ? (a.tok / 2 + 15) & ~15 : 0;
-        const int most = (warp >> 2) & 1 ? QW_TOK : (a.tok / 2 + 15) & ~15;
+        const int first = warp >= 16 ? (a.tok / 2 + 15) & ~15 : 0;
+        const int most = warp >= 16 ? QW_TOK : (a.tok / 2 + 15) & ~15;
         uint32_t d = 0, ph = 0;
         for (int t = blockIdx.x; t < total; t += gridDim.x) {
             const int m = t / a.tts * QW_ROWS + q * 32 + lane, n0 = t % a.tts * a.tok;
@@ -1077,17 +1082,15 @@ __global__ void __launch_bounds__(QW_THREADS, 1)
                     if (u && gi >= groups) break;
                     const float s = __bfloat162float(gi & 2 ? (gi & 1 ? sc[3] : sc[2]) : (gi & 1 ? sc[1] : sc[0]));
                     const uint32_t base = tmem_base + (d * BATCH + u) * a.ld + first + ((uint32_t)(q * 32) << 16);
-                    uint32_t v[48];
-#pragma unroll
-                    for (int c = 0; c < 3; ++c)
-                        if (cnt > c * 16) tmem_ld_32x32b_x16(base + c * 16, v + c * 16);
-                    tmem_ld_wait();
 #pragma unroll
                     for (int c = 0; c < 3; ++c)
                         if (cnt > c * 16) {
+                            uint32_t v[16];
+                            tmem_ld_32x32b_x16(base + c * 16, v);
+                            tmem_ld_wait();
 #pragma unroll
                             for (int j = 0; j < 16; ++j)
-                                acc[c * 16 + j] = fmaf(s, __uint_as_float(v[c * 16 + j]), acc[c * 16 + j]);
+                                acc[c * 16 + j] = fmaf(s, __uint_as_float(v[j]), acc[c * 16 + j]);
                         }
                 }
                 tc_fence_before();
