@@ -1120,33 +1120,47 @@ __global__ void __launch_bounds__(QW_THREADS, 1)
 }
 
 // y(n) = the k weighted expert rows in slot order + the shared expert's row, fp32,
-// rounded once.  One thread per 8 columns.
-__global__ void __launch_bounds__(128) quant_combine_kernel(const QuantArgs a, const float *slot,
-                                                            const float *osh, const int32_t *pos_of,
-                                                            __nv_bfloat16 *y, int D) {
+// rounded once.  One thread per 4 columns; eight rows are fetched before any is added (a
+// row after the other, each behind its position's load, took 9 us for 16 tokens).
+constexpr int QC_THREADS = 128;
+__global__ void __launch_bounds__(QC_THREADS) quant_combine_kernel(const QuantArgs a, const float *slot,
+                                                                   const float *osh, const int32_t *pos_of,
+                                                                   __nv_bfloat16 *y, int D) {
     grid_dep_wait();
-    const int n = blockIdx.x, c = (blockIdx.y * 128 + threadIdx.x) * 8;
+    const int n = blockIdx.x, c = (blockIdx.y * QC_THREADS + threadIdx.x) * 4;
     if (c >= D) return;
-    float v[8] = {};
-    for (int j = 0; j < a.k; ++j) {
-        int p;
-        if (a.direct) {
-            const int e = a.topk_idx[j];
-            p = e >= 0 && e < a.E ? j : -1;
-        } else {
-            p = pos_of[(size_t)n * a.k + j];
+    const float4 o = __ldcg(reinterpret_cast<const float4 *>(osh + (size_t)n * D + c));
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int j0 = 0; j0 < a.k; j0 += 8) {
+        int p[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            p[j] = -1;
+            if (j0 + j < a.k) {
+                if (a.direct) {
+                    const int e = a.topk_idx[j0 + j];
+                    if (e >= 0 && e < a.E) p[j] = j0 + j;
+                } else {
+                    p[j] = pos_of[(size_t)n * a.k + j0 + j];
+                }
+            }
         }
-        if (p < 0) continue;
-        const float4 *s = reinterpret_cast<const float4 *>(slot + (size_t)p * D + c);
-        const float4 lo = __ldcg(s), hi = __ldcg(s + 1);
-        v[0] += lo.x; v[1] += lo.y; v[2] += lo.z; v[3] += lo.w;
-        v[4] += hi.x; v[5] += hi.y; v[6] += hi.z; v[7] += hi.w;
+        float4 w[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            w[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (p[j] >= 0) w[j] = __ldcg(reinterpret_cast<const float4 *>(slot + (size_t)p[j] * D + c));
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            v.x += w[j].x;
+            v.y += w[j].y;
+            v.z += w[j].z;
+            v.w += w[j].w;
+        }
     }
-    const float4 *o = reinterpret_cast<const float4 *>(osh + (size_t)n * D + c);
-    const float4 lo = __ldcg(o), hi = __ldcg(o + 1);
-    *reinterpret_cast<uint4 *>(y + (size_t)n * D + c) =
-        make_uint4(pack_bf16x2(v[0] + lo.x, v[1] + lo.y), pack_bf16x2(v[2] + lo.z, v[3] + lo.w),
-                   pack_bf16x2(v[4] + hi.x, v[5] + hi.y), pack_bf16x2(v[6] + hi.z, v[7] + hi.w));
+    *reinterpret_cast<uint2 *>(y + (size_t)n * D + c) =
+        make_uint2(pack_bf16x2(v.x + o.x, v.y + o.y), pack_bf16x2(v.z + o.z, v.w + o.w));
 }
 
 }  // namespace moe

@@ -427,7 +427,7 @@ int moe_forward_quant(const void *x, const void *gate_up, const void *gate_up_sc
          : W.tile_rows == 16 ? quant_layer_t<8, 2, 128, 2>(w, a, x, ws, W, dev, prof, st)
                              : quant_layer_t<8, 2, 128, 4>(w, a, x, ws, W, dev, prof, st);
     if (rc != MOE_OK) return rc;
-    rc = launch_serial(quant_combine_kernel, dim3(N, (D + 1023) / 1024, 1), 128, 0, st, a,
+    rc = launch_serial(quant_combine_kernel, dim3(N, (D + 4 * QC_THREADS - 1) / (4 * QC_THREADS), 1), QC_THREADS, 0, st, a,
                        (const float *)(ws + W.slot), (const float *)(ws + W.osh), (const int32_t *)dp.pos_of,
                        static_cast<__nv_bfloat16 *>(y), D);
     prof.mark();
