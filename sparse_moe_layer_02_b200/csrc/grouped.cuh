@@ -467,16 +467,18 @@ __global__ void __launch_bounds__(GrpCfg<MODE>::THREADS, 1)
 }
 
 // ---------------------------------------------------------------------------
-// fp32: the same three products on the CUDA cores, T x T output tiles, 32 summed
-// indices at a time in shared memory, 4 x 4 sums a thread (fp32, one running sum in
-// index order); the next 32 are on their way from memory meanwhile.  The summed index
-// never crosses a segment, so nothing is masked but loads.  T = 64 for large batches, 32
-// for small ones (more tiles for the same SMs).
+// fp32: the same three products on the CUDA cores, T x T output tiles, KB summed indices
+// at a time in shared memory, fp32 sums in registers, one running sum each, in index
+// order; the next KB are on their way from memory meanwhile.  The summed index never
+// crosses a segment, so nothing is masked but loads.  Large batches take T = 64 with
+// 8 x 8 sums a thread (four 16-byte shared loads for 64 multiply-adds; with 4 x 4 the
+// shared memory's bandwidth is the bound), small ones T = 32 with 4 x 4: more tiles for
+// the same SMs.
 // ---------------------------------------------------------------------------
 // Element (k, i) of an operand in shared memory; loads are 16 bytes along the contiguous
 // index: the summed one (KCONT) or the other.
-template <bool KCONT, int T, int NT> struct F32Operand {
-    static constexpr int KB = 32, PER = KB * T / 4 / NT; // pieces of a thread
+template <bool KCONT, int T, int KB, int NT> struct F32Operand {
+    static constexpr int PER = KB * T / 4 / NT; // pieces of a thread
     float4 v[PER];
     // rows: of the contiguous direction's other index; ld: elements from one to the next
     __device__ __forceinline__ void load(const float *p, size_t ld, int nk, int ni, int tid) {
@@ -506,10 +508,16 @@ template <bool KCONT, int T, int NT> struct F32Operand {
     }
 };
 
+template <int T> struct GrpF32 {
+    static constexpr int SUMS = T == 64 ? 8 : 4; // of a thread, in each direction
+    static constexpr int KB = T == 64 ? 16 : 32;
+    static constexpr int THREADS = (T / SUMS) * (T / SUMS);
+};
+
 template <int MODE, int T>
-__global__ void __launch_bounds__((T / 4) * (T / 4)) grouped_f32_kernel(const float *A, const float *B,
-                                                                        const GroupedArgs a) {
-    constexpr int NT = (T / 4) * (T / 4), KB = 32;
+__global__ void __launch_bounds__(GrpF32<T>::THREADS) grouped_f32_kernel(const float *A, const float *B,
+                                                                         const GroupedArgs a) {
+    constexpr int S = GrpF32<T>::SUMS, NT = GrpF32<T>::THREADS, KB = GrpF32<T>::KB, H = S / 4;
     __shared__ __align__(16) float sA[KB][T + 4], sB[KB][T + 4];
     __shared__ int s_off[GRP_MAXE + 1], s_tile[GRP_MAXE + 1];
     const int tid = threadIdx.x;
@@ -518,7 +526,7 @@ __global__ void __launch_bounds__((T / 4) * (T / 4)) grouped_f32_kernel(const fl
     if (tid < 32) grouped_table(a.offsets, a.E, a.rows, T, s_off, s_tile, blockIdx.x == 0, tid);
     __syncthreads();
     const int total = MODE == GRP_WGRAD ? a.E * a.nb * a.mb : s_tile[a.E] * a.nb;
-    const int tx = tid % (T / 4), ty = tid / (T / 4);
+    const int tx = tid % (T / S), ty = tid / (T / S); // places 4 tx.. (and T/2 + 4 tx..), 4 ty..
     float *out = static_cast<float *>(a.out);
     for (int t = blockIdx.x; t < total; t += gridDim.x) {
         int e, i0, i1, n0, r0, red;
@@ -541,8 +549,8 @@ __global__ void __launch_bounds__((T / 4) * (T / 4)) grouped_f32_kernel(const fl
             red = a.red;
         }
         const float *We = B + (size_t)e * a.M * a.K; // forward, dgrad
-        F32Operand<MODE != GRP_WGRAD, T, NT> fa;     // forward x[i][k], dgrad dy[i][k], wgrad dy[r0+k][i]
-        F32Operand<MODE == GRP_FORWARD, T, NT> fb;   // forward W[n][k], dgrad W[k][n], wgrad x[r0+k][n]
+        F32Operand<MODE != GRP_WGRAD, T, KB, NT> fa;     // forward x[i][k], dgrad dy[i][k], wgrad dy[r0+k][i]
+        F32Operand<MODE == GRP_FORWARD, T, KB, NT> fb;   // forward W[n][k], dgrad W[k][n], wgrad x[r0+k][n]
         auto fetch = [&](int k0) {
             if (MODE == GRP_WGRAD) {
                 fa.load(A + (size_t)(r0 + k0) * a.M + i0, a.M, red - k0, i1 - i0, tid);
@@ -555,7 +563,7 @@ __global__ void __launch_bounds__((T / 4) * (T / 4)) grouped_f32_kernel(const fl
                     fb.load(We + (size_t)k0 * a.K + n0, a.K, red - k0, a.ncols - n0, tid);
             }
         };
-        float acc[4][4] = {};
+        float acc[S][S] = {};
         if (red > 0) fetch(0);
         for (int k0 = 0; k0 < red; k0 += KB) {
             fa.store(sA, tid);
@@ -564,25 +572,32 @@ __global__ void __launch_bounds__((T / 4) * (T / 4)) grouped_f32_kernel(const fl
             if (k0 + KB < red) fetch(k0 + KB);
 #pragma unroll 8
             for (int k = 0; k < KB; ++k) {
-                const float4 x = *reinterpret_cast<const float4 *>(&sA[k][ty * 4]);
-                const float4 w = *reinterpret_cast<const float4 *>(&sB[k][tx * 4]);
-                const float xa[4] = {x.x, x.y, x.z, x.w}, wb[4] = {w.x, w.y, w.z, w.w};
+                float xa[S], wb[S];
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
+                for (int h = 0; h < H; ++h) {
+                    const float4 x = *reinterpret_cast<const float4 *>(&sA[k][h * (T / 2) + ty * 4]);
+                    const float4 w = *reinterpret_cast<const float4 *>(&sB[k][h * (T / 2) + tx * 4]);
+                    xa[4 * h] = x.x, xa[4 * h + 1] = x.y, xa[4 * h + 2] = x.z, xa[4 * h + 3] = x.w;
+                    wb[4 * h] = w.x, wb[4 * h + 1] = w.y, wb[4 * h + 2] = w.z, wb[4 * h + 3] = w.w;
+                }
 #pragma unroll
-                    for (int n = 0; n < 4; ++n) acc[i][n] = fmaf(xa[i], wb[n], acc[i][n]);
+                for (int i = 0; i < S; ++i)
+#pragma unroll
+                    for (int n = 0; n < S; ++n) acc[i][n] = fmaf(xa[i], wb[n], acc[i][n]);
             }
             __syncthreads();
         }
-        const int n = n0 + tx * 4;
-        if (n < a.ncols) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int row = i0 + ty * 4 + i;
+        for (int h = 0; h < H; ++h) {
+            const int n = n0 + h * (T / 2) + tx * 4;
+            if (n >= a.ncols) break;
+#pragma unroll
+            for (int i = 0; i < S; ++i) {
+                const int row = i0 + (i / 4) * (T / 2) + ty * 4 + i % 4;
                 if (row < i1) {
                     const size_t at = MODE == GRP_WGRAD ? (size_t)e * a.M + row : (size_t)row;
                     *reinterpret_cast<float4 *>(out + at * a.ncols + n) =
-                        make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+                        make_float4(acc[i][4 * h], acc[i][4 * h + 1], acc[i][4 * h + 2], acc[i][4 * h + 3]);
                 }
             }
         }

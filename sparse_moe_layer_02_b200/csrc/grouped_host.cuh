@@ -127,8 +127,8 @@ int grouped_impl(const void *A, const void *B, const int32_t *offsets, int rows,
                                                : ((size_t)rows / T + std::min(rows, E)) * a.nb;
         const int grid = (int)std::min<size_t>(std::max<size_t>(tiles, 1), (size_t)dev->sms * 8);
         const float *fa = static_cast<const float *>(A), *fb = static_cast<const float *>(B);
-        if (small) return launch_serial(grouped_f32_kernel<MODE, 32>, dim3(grid, 1, 1), 64, 0, st, fa, fb, a);
-        return launch_serial(grouped_f32_kernel<MODE, 64>, dim3(grid, 1, 1), 256, 0, st, fa, fb, a);
+        if (small) return launch_serial(grouped_f32_kernel<MODE, 32>, dim3(grid, 1, 1), GrpF32<32>::THREADS, 0, st, fa, fb, a);
+        return launch_serial(grouped_f32_kernel<MODE, 64>, dim3(grid, 1, 1), GrpF32<64>::THREADS, 0, st, fa, fb, a);
     }
 
     a.nb = (a.ncols + GRP_BN - 1) / GRP_BN;
