@@ -334,7 +334,8 @@ int moe_grouped_linear_wgrad(const void *dy, const void *x, const int32_t *offse
  *   are not rounded to bf16: codes times tokens are summed in fp32 per group, the
  *   scale applied in fp32, y rounded once.  Made for N up to a few hundred; any N
  *   works.  N = 0 is a no-op.  Tokens of magnitude 2^63 and scales of 2^58 and more
- *   count as infinite (as in moe_forward_quant, the SwiGLU output included).
+ *   may count as infinite (in moe_forward_quant too, the SwiGLU output included); what an
+ *   infinite or NaN token or scale gives is infinite or NaN, in its own outputs only.
  *
  * moe_forward_quant: moe_forward (with moe_forward_clamped's limits; +infinity for
  *   none) on bf16 tokens with every expert in 4 bits: gate_up [E, 2 d_moe, D], gate

@@ -6,6 +6,7 @@
 
 moe_grouped_linear takes part in autograd.  Every call runs on the tensors' own device,
 on that device's current stream unless a stream is given, and needs all tensors there.
+What a call makes belongs, as torch's allocator sees it, to the stream the call runs on.
 """
 
 from __future__ import annotations
@@ -44,13 +45,14 @@ def _device(*tensors):
     return dev
 
 
+def _handle(stream):
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else stream
+
+
 def _call(name, dev, stream, *args):
     """One library call on device dev, with the stream as its last argument."""
     f = getattr(load_library(), name)
-    if stream is None:
-        stream = _current_stream(dev)
-    elif isinstance(stream, torch.cuda.Stream):
-        stream = stream.cuda_stream
+    stream = _current_stream(dev) if stream is None else _handle(stream)
     if dev == torch.cuda.current_device():
         rc = f(*args, stream)
     else:
@@ -60,10 +62,20 @@ def _call(name, dev, stream, *args):
         _check(rc, name)
 
 
-def _out(t, shape, dtype, like, name):
-    """An output the caller gave, checked, or a new one (unset) on the device of `like`."""
-    if t is None:
+def _new(shape, dtype, like, stream):
+    """A tensor (unset) on the device of `like` for a call on `stream`.  It is taken from that
+    stream's memory: a block that the current stream has given back may still be in use
+    there, and one that this call gives back is still in use here."""
+    if stream is None:
         return like.new_empty(shape, dtype=dtype)
+    with torch.cuda.stream(torch.cuda.ExternalStream(_handle(stream), device=like.device)):
+        return like.new_empty(shape, dtype=dtype)
+
+
+def _out(t, shape, dtype, like, name, stream):
+    """An output the caller gave, checked, or a new one."""
+    if t is None:
+        return _new(shape, dtype, like, stream)
     if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.get_device() != like.get_device() \
             or not t.is_contiguous():
         raise ValueError("%s must be contiguous, %s %s on the inputs' device" % (name, list(shape), dtype))
@@ -89,7 +101,7 @@ def _linear(x, W, offsets, y, stream):
     (rows, K), (E, M, _) = x.shape, W.shape
     _check_offsets(offsets, E)
     rest = int(y is None)
-    y = _out(y, (rows, M), x.dtype, x, "y")
+    y = _out(y, (rows, M), x.dtype, x, "y", stream)
     _call("moe_grouped_linear", dev, stream, x.data_ptr(), W.data_ptr(), offsets.data_ptr(), rows,
           E, M, K, _dt(x), y.data_ptr(), rest)
     return y
@@ -162,7 +174,7 @@ def moe_grouped_linear_dgrad(dy, W, offsets, dx=None, stream=None):
     rows, (E, M, K) = dy.shape[0], W.shape
     _check_offsets(offsets, E)
     rest = int(dx is None)
-    dx = _out(dx, (rows, K), dy.dtype, dy, "dx")
+    dx = _out(dx, (rows, K), dy.dtype, dy, "dx", stream)
     _call("moe_grouped_linear_dgrad", dev, stream, dy.data_ptr(), W.data_ptr(), offsets.data_ptr(),
           rows, E, M, K, _dt(dy), dx.data_ptr(), rest)
     return dx
@@ -177,7 +189,7 @@ def moe_grouped_linear_wgrad(dy, x, offsets, dW=None, stream=None):
     _same_type(dy, x)
     (rows, M), K, E = dy.shape, x.shape[1], offsets.shape[0] - 1
     _check_offsets(offsets, E)
-    dW = _out(dW, (E, M, K), dy.dtype, dy, "dW")
+    dW = _out(dW, (E, M, K), dy.dtype, dy, "dW", stream)
     _call("moe_grouped_linear_wgrad", dev, stream, dy.data_ptr(), x.data_ptr(), offsets.data_ptr(),
           rows, E, M, K, _dt(dy), dW.data_ptr())
     return dW

@@ -9,7 +9,8 @@ A matrix [M, K] is a pair (q, scales): q uint8 [M, K/2], column 2j in the low an
 the high four bits of byte j, scales bf16 [K/group, M]; its value at (m, k) is
 (code - 8) * scales[k // group, m].  The group size is read off the shapes.
 Every call runs on the tensors' own device, on that device's current stream unless a
-stream is given, and needs all tensors there.
+stream is given, and needs all tensors there.  What a call makes belongs, as torch's
+allocator sees it, to the stream the call runs on.  No call takes part in autograd.
 """
 
 from __future__ import annotations
@@ -17,7 +18,7 @@ from __future__ import annotations
 import torch
 
 from . import load_library
-from .products import _call, _device, _out
+from .products import _call, _device, _new, _out
 
 __all__ = ["moe_quantize", "moe_dequantize", "moe_linear_quant", "moe_forward_quant",
            "moe_forward_quant_workspace"]
@@ -28,7 +29,7 @@ def _pair(q, scales, lead, name):
     if q.dtype != torch.uint8 or scales.dtype != torch.bfloat16:
         raise ValueError("%s must be (uint8 codes, bfloat16 scales)" % name)
     qs, ss = q.shape, scales.shape
-    if len(qs) == lead + 2 and len(ss) == lead + 2 and qs[:lead] == ss[:lead]:
+    if lead >= 0 and len(qs) == lead + 2 and len(ss) == lead + 2 and qs[:lead] == ss[:lead]:
         M, K, groups = qs[lead], 2 * qs[lead + 1], ss[lead]
         if ss[lead + 1] == M and groups and not K % groups:
             return M, K, K // groups
@@ -43,8 +44,8 @@ def moe_quantize(W, group: int = 128, q=None, scales=None, stream=None):
     lead, (M, K) = tuple(W.shape[:-2]), W.shape[-2:]
     if group not in (32, 64, 128) or K % group:
         raise ValueError("group must be 32, 64 or 128 and divide K")
-    q = _out(q, lead + (M, K // 2), torch.uint8, W, "q")
-    scales = _out(scales, lead + (K // group, M), torch.bfloat16, W, "scales")
+    q = _out(q, lead + (M, K // 2), torch.uint8, W, "q", stream)
+    scales = _out(scales, lead + (K // group, M), torch.bfloat16, W, "scales", stream)
     E = W.numel() // (M * K) if M * K else 0
     _call("moe_quantize", dev, stream, W.data_ptr(), E, M, K, group, q.data_ptr(), scales.data_ptr())
     return q, scales
@@ -54,7 +55,7 @@ def moe_dequantize(q, scales, W=None, stream=None):
     """The bf16 values [..., M, K] of 4-bit weights."""
     M, K, group = _pair(q, scales, q.dim() - 2, "the weights")
     dev = _device(q, scales)
-    W = _out(W, tuple(q.shape[:-2]) + (M, K), torch.bfloat16, q, "W")
+    W = _out(W, tuple(q.shape[:-2]) + (M, K), torch.bfloat16, q, "W", stream)
     E = W.numel() // (M * K) if M * K else 0
     _call("moe_dequantize", dev, stream, q.data_ptr(), scales.data_ptr(), E, M, K, group, W.data_ptr())
     return W
@@ -67,7 +68,7 @@ def moe_linear_quant(x, q, scales, y=None, stream=None):
         raise ValueError("x must be bfloat16 [N, K]")
     dev = _device(x, q, scales)
     N = x.shape[0]
-    y = _out(y, (N, M), torch.bfloat16, x, "y")
+    y = _out(y, (N, M), torch.bfloat16, x, "y", stream)
     _call("moe_linear_quant", dev, stream, x.data_ptr(), q.data_ptr(), scales.data_ptr(), N, M, K,
           group, y.data_ptr())
     return y
@@ -102,10 +103,10 @@ def moe_forward_quant(x, gate_up, down, sh_gate_up, sh_down, topk_idx, topk_w, y
         raise ValueError("topk_idx must be int32 and topk_w float32, both [N, k]")
     k = topk_idx.shape[1]
     dev = _device(x, *gate_up, *down, *sh_gate_up, *sh_down, topk_idx, topk_w)
-    y = _out(y, (N, D), torch.bfloat16, x, "y")
+    y = _out(y, (N, D), torch.bfloat16, x, "y", stream)
     if workspace is None:
-        workspace = x.new_empty(max(moe_forward_quant_workspace(N, D, E, d, d_sh, k), 256),
-                                dtype=torch.uint8)
+        workspace = _new((max(moe_forward_quant_workspace(N, D, E, d, d_sh, k), 256),),
+                         torch.uint8, x, stream)
     elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError("the workspace must be contiguous, on the inputs' device")
     inf = float("inf")

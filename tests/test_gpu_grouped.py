@@ -338,3 +338,22 @@ def test_two_streams_at_once():
     torch.cuda.synchronize()
     assert all(torch.equal(y, want[i]) for i in range(2) for y in got[i])
     assert moe.moe_device_status() == 0
+
+
+def test_what_a_call_makes_is_memory_of_the_calls_stream():
+    # The current stream gives a block back while its last write is still to come; a call on
+    # another stream must not be handed that block.
+    x, W, dy, off = _case([200, 3, 130], 1288, 2056, BF16)
+    other = torch.cuda.Stream()
+    for f in (lambda **k: moe.moe_grouped_linear(x, W, off, **k),
+              lambda **k: moe.moe_grouped_linear_dgrad(dy, W, off, **k),
+              lambda **k: moe.moe_grouped_linear_wgrad(dy, x, off, **k)):
+        want = f()
+        torch.cuda.synchronize()
+        scratch = torch.empty_like(want)
+        torch.cuda._sleep(100_000_000)
+        scratch.fill_(float("nan"))
+        del scratch
+        got = f(stream=other)
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)

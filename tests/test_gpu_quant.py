@@ -410,3 +410,30 @@ def test_two_streams_at_once():
             for i in range(2)] for _ in range(20)]
     torch.cuda.synchronize()
     assert all(torch.equal(y[i], want[i]) for y in got for i in range(2))
+
+
+def test_what_a_call_makes_is_memory_of_the_calls_stream():
+    # The current stream gives a block back while its last write is still to come; a call on
+    # another stream must not be handed that block.
+    g = _gen(13)
+    W = _randn(g, 2048, 512, std=0.02)
+    q, s = moe.moe_quantize(W, 64)
+    x = _randn(g, 300, 512)
+    other = torch.cuda.Stream()
+    for f in (lambda **k: moe.moe_linear_quant(x, q, s, **k), lambda **k: moe.moe_dequantize(q, s, **k)):
+        want = f()
+        for stream in (other, other.cuda_stream):
+            torch.cuda.synchronize()
+            scratch = torch.empty_like(want)
+            torch.cuda._sleep(100_000_000)
+            scratch.fill_(float("nan"))
+            del scratch
+            got = f(stream=stream)
+            torch.cuda.synchronize()
+            assert torch.equal(got, want)
+    x, w, ids, tw = _layer(12, 256, 6, 2, 128, 128, 64)
+    want = _run(x, w, ids, tw)
+    torch.cuda.synchronize()
+    got = [_run(x, w, ids, tw, stream=other) for _ in range(4)]  # workspaces taken and given back there
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, want) for y in got)
