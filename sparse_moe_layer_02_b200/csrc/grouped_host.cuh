@@ -118,8 +118,15 @@ int grouped_impl(const void *A, const void *B, const int32_t *offsets, int rows,
     a.wait_limit_ns = g_wait_limit_ns;
 
     if (dtype == MOE_F32) {
-        // Small batches have too few 64-row tiles for the SMs.
-        const bool small = ((size_t)rows / 64 + 1) * (ncols / 64 + 1) < (size_t)dev->sms;
+        // 64 x 64 tiles need less shared memory traffic, 32 x 32 tiles spread few rows over
+        // the SMs (us, 32 / 64): forward, 256 rows, 16 x 256 x 256 9.7 / 18.7; 1024 rows,
+        // 8 x 512 x 512 (128 tiles of 64) 28 / 37; 1500 rows, 20 x 512 x 900 (190 tiles)
+        // 93 / 104, its dgrad (345) 107 / 84; 4000 rows, 8 x 1024 x 1024 368 / 231.  wgrad,
+        // whose tiles do not depend on the rows: 4 x 256 x 256 (64) 3.6 / 3.7,
+        // 16 x 256 x 256 (256) 5.9 / 4.1, 16 x 512 x 512 26 / 16.
+        const size_t large = MODE == GRP_WGRAD ? (size_t)E * ((M + 63) / 64) * ((K + 63) / 64)
+                                               : (size_t)rows * ncols / (64 * 64);
+        const bool small = 2 * large < (MODE == GRP_WGRAD ? 1 : 3) * (size_t)dev->sms;
         const int T = small ? 32 : 64;
         a.nb = (a.ncols + T - 1) / T;
         a.mb = (M + T - 1) / T;
@@ -139,7 +146,7 @@ int grouped_impl(const void *A, const void *B, const int32_t *offsets, int rows,
         ok = make_map(&mA, A, K, rows, K, GRP_BM) && make_map3(&mB, B, K, M, E, 64, GRP_BN) &&
              make_map(&mOut, out, M, rows, M, 32);
     else if (MODE == GRP_DGRAD) {
-        a.wide = K % 64 == 0;
+        a.wide = K % 64 == 0; // (dgrad 16384 rows, 32 x 4096 x 6144: 744 us, 749 without; wgrad 915, 923)
         ok = make_map(&mA, A, M, rows, M, GRP_BM) && make_map(&mOut, out, K, rows, K, 32) &&
              (a.wide ? make_map_blocks(&mB, B, K, M, E, 64, 4, true) : make_map3(&mB, B, K, M, E, 64, 64));
     } else {
