@@ -201,7 +201,7 @@ template <int RG, int MT, int KW, int NT, int G> struct QmCfg {
     static constexpr int R = 16 * MT * RG, HALF = R / 2; // weight rows of a tile
     static constexpr int SK = KW * KS;              // columns of a stage
     static constexpr int UNIT = G < KW ? G : KW;    // columns of a slice under one scale
-    static constexpr int BLOCKS = NT <= 2 ? 2 : 1; // per SM
+    static constexpr int BLOCKS = 2; // per SM
     static constexpr int BOX = SK / 2 < 128 ? SK / 2 : 128; // bytes of a code box's row = swizzle span
     static constexpr int NBOX = SK / 2 / BOX;
     static constexpr int W_BYTES = R * SK / 2;
@@ -586,11 +586,10 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<RG, MT, KW, NT, G>::BLOCKS)
             QuantTile c;
             if (!quant_tile<KIND, TT>(t, routed, a, s_tile, s_cnt, c)) continue;
             const int K = c.shared ? a.K_s : a.K;
-            const int nt = (c.cnt + 7) >> 3;
             const int stages = (K + SK - 1) / SK;
             bool ok = true;
-            // The tile's sums for NTT blocks of 8 tokens (blocks past nt hold anything: a
-            // column of the product depends on its own token only).
+            // The tile's sums for NTT blocks of 8 tokens (tokens past cnt hold
+            // anything: a column of the product depends on its own token only).
             auto sums = [&](auto ntt) {
                 constexpr int NTT = decltype(ntt)::value;
                 float acc[MT][NTT][4];
@@ -700,10 +699,8 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<RG, MT, KW, NT, G>::BLOCKS)
                         }
                 }
             };
-            if (NT == 1 || nt == 1)
+            if (c.cnt <= 8)
                 sums(IntC<1>{});
-            else if (NT == 2 || nt == 2)
-                sums(IntC<NT < 2 ? NT : 2>{});
             else
                 sums(IntC<NT>{});
             if (KS == 1) continue;
@@ -766,7 +763,10 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<RG, MT, KW, NT, G>::BLOCKS)
 // ---------------------------------------------------------------------------
 // The product of one matrix with more than 16 tokens.  There the register kernel's MMA
 // time grows with the tokens (mma.sync m16n8k16, 8 cycles each), so tcgen05 takes over:
-// a tile is 128 weight rows x up to 96 tokens, one block per SM.
+// a tile is 128 weight rows x up to 96 tokens, one block per SM.  Where that leaves SMs
+// idle, the blocks of a cluster share a tile's columns: each sums its own, hands every
+// block its tokens' sums through distributed shared memory, and those are added in the
+// blocks' order.
 //
 //   warp 0       TMA producer of the codes: 128 columns (8 KiB) a stage
 //   warp 2       TMA producer of the tokens: two swizzled boxes of 64 columns a stage
@@ -795,8 +795,9 @@ constexpr int QW_UCOL = 512 - QW_UST * QW_COLS / 2;
 constexpr int QW_MAXACC = 12; // TMEM accumulators in turn: QW_UCOL columns / tokens of a tile
 constexpr int QW_C_BYTES = QW_ROWS * QW_COLS / 2;     // 8 KiB of codes
 constexpr int QW_X_HALF = QW_TOK * 128;               // 64 columns of the tokens
-constexpr int QW_X_BYTES = 2 * QW_X_HALF;             // 32 KiB
-constexpr int QW_SMEM = 1024 + QW_CST * QW_C_BYTES + QW_AST * QW_X_BYTES + 768;
+constexpr int QW_X_BYTES = 2 * QW_X_HALF;             // 24 KiB
+constexpr int QW_JOIN = QW_TOK + 8; // sums of a row from a cluster's blocks, each its share rounded up
+constexpr int QW_SMEM = 1024 + QW_CST * QW_C_BYTES + QW_AST * QW_X_BYTES + QW_JOIN * QW_ROWS * 4 + 768;
 static_assert(QW_SMEM <= 232448, "shared memory");
 constexpr int QW_UNPACK = 4, QW_SUMS = 8;             // warps
 
@@ -842,12 +843,15 @@ struct QuantWideArgs {
     int tok;        // tokens of a tile (a multiple of 16)
     int accs, ld;   // batches of TMEM accumulators; columns of one
     int nb, tts;    // row tiles, token tiles
+    int split, own; // blocks of a cluster that share a tile's columns; tokens each finishes
     uint64_t wait_limit_ns;
 };
 
 // Maps: mC codes [M, K/2] bytes, box 64 x 128, swizzled; mX tokens [N, K], box 64 x
 // the tile's tokens, swizzled (large boxes: each TMA load costs its issuer 75-150 cycles).
-template <int G>
+// SPLIT: the blocks of a cluster share a tile's columns (a kernel of its own, as one for
+// both ran 4 to 15 % slower unshared).
+template <int G, bool SPLIT>
 __global__ void __launch_bounds__(QW_THREADS, 1)
     quant_wide_kernel(const __grid_constant__ CUtensorMap mC, const __grid_constant__ CUtensorMap mX,
                       const QuantWideArgs a) {
@@ -858,11 +862,13 @@ __global__ void __launch_bounds__(QW_THREADS, 1)
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     uint8_t *cbuf = smem;
     uint8_t *xbuf = cbuf + QW_CST * QW_C_BYTES;
-    uint64_t *cfull = reinterpret_cast<uint64_t *>(xbuf + QW_AST * QW_X_BYTES);
+    float *join = reinterpret_cast<float *>(xbuf + QW_AST * QW_X_BYTES); // [block][token][row]
+    uint64_t *cfull = reinterpret_cast<uint64_t *>(join + QW_JOIN * QW_ROWS);
     uint64_t *cempty = cfull + QW_CST;
     uint64_t *afull = cempty + QW_CST, *aempty = afull + QW_AST;
     uint64_t *uempty = aempty + QW_AST, *dfull = uempty + QW_UST, *dempty = dfull + QW_MAXACC, *drain = dempty + QW_MAXACC;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 2);
+    uint64_t *jfull = drain + 2, *jempty = jfull + 1;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(jempty + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     const int warp = warp_id(), lane = lane_id();
 
@@ -881,6 +887,10 @@ __global__ void __launch_bounds__(QW_THREADS, 1)
             mbar_init(&dempty[i], QW_SUMS);
         }
         for (int i = 0; i < 2; ++i) mbar_init(&drain[i], 1);
+        if (SPLIT) {
+            mbar_init(jfull, QW_SUMS * a.split);
+            mbar_init(jempty, QW_SUMS * a.split);
+        }
         *abort_flag = 0;
         fence_mbar_init();
         tma_prefetch_desc(&mC);
@@ -894,11 +904,19 @@ __global__ void __launch_bounds__(QW_THREADS, 1)
         tmem_relinquish();
     }
     tc_fence_before();
-    __syncthreads();
+    if (SPLIT)
+        cluster_sync_all(); // every block's barriers are ready for the others' arrivals
+    else
+        __syncthreads();
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
     const int total = a.nb * a.tts; // token tiles of one row tile are neighbours
-    const int stages = (a.K + QW_COLS - 1) / QW_COLS, groups = a.K / G;
+    const int split = SPLIT ? a.split : 1, rank = SPLIT ? (int)cluster_ctarank() : 0;
+    const int tile0 = blockIdx.x / split, step = gridDim.x / split;
+    // this block's stages and groups of a tile
+    const int all = (a.K + QW_COLS - 1) / QW_COLS;
+    const int st0 = all * rank / split, st1 = all * (rank + 1) / split;
+    const int gr0 = st0 * GROUPS, groups = min(st1 * GROUPS, a.K / G) - gr0;
     const uint64_t limit = a.wait_limit_ns;
 
     if (warp == 0 || warp == 2) {
@@ -908,9 +926,9 @@ __global__ void __launch_bounds__(QW_THREADS, 1)
             const uint32_t ring = codes ? QW_CST : QW_AST;
             uint32_t it = 0, s = 0, ph = 0;
             bool ok = true;
-            for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+            for (int t = tile0; t < total && ok; t += step) {
                 const int m0 = t / a.tts * QW_ROWS, n0 = t % a.tts * a.tok;
-                for (int i = 0; i < stages; ++i, ++it) {
+                for (int i = st0; i < st1; ++i, ++it) {
                     if (!mbar_wait(&empty[s], ph ^ 1, limit, abort_flag, codes ? 501 : 503)) { ok = false; break; }
                     if (codes) {
                         mbar_arrive_expect_tx(&full[s], QW_C_BYTES);
@@ -949,10 +967,10 @@ __global__ void __launch_bounds__(QW_THREADS, 1)
                     ph ^= 1;
                 }
             };
-            for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+            for (int t = tile0; t < total && ok; t += step) {
                 const int n = (min(a.tok, a.N - t % a.tts * a.tok) + 15) & ~15;
                 const uint32_t idesc = umma_idesc_bf16(QW_ROWS, n);
-                for (int i = 0; i < stages && ok; ++i, ++it) {
+                for (int i = 0; i < st1 - st0 && ok; ++i, ++it) {
                     const int ng = min(GROUPS, groups - i * GROUPS);
                     if ((it & 1) != turn) {
                         // The other's stage.  A wait must not fall two rounds behind its
@@ -1002,8 +1020,8 @@ __global__ void __launch_bounds__(QW_THREADS, 1)
         const uint32_t ta = tmem_base + QW_UCOL + ((uint32_t)(q * 32) << 16);
         uint32_t it = 0;
         bool ok = true;
-        for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
-            for (int i = 0; i < stages; ++i, ++it) {
+        for (int t = tile0; t < total && ok; t += step) {
+            for (int i = st0; i < st1; ++i, ++it) {
                 if ((int)(it & 1) != team) continue;
                 const uint32_t s = it % QW_CST, b = it % QW_AST, u = it % QW_UST;
                 ok = mbar_wait(&cfull[s], (it / QW_CST) & 1, limit, abort_flag, 521);
@@ -1050,11 +1068,11 @@ __global__ void __launch_bounds__(QW_THREADS, 1)
         // this warp's tokens of the tile: the first or the second half, in steps of 16
         const int first = warp >= 16 ? (a.tok / 2 + 15) & ~15 : 0;
         const int most = warp >= 16 ? QW_TOK : (a.tok / 2 + 15) & ~15;
-        uint32_t d = 0, ph = 0;
-        for (int t = blockIdx.x; t < total; t += gridDim.x) {
+        uint32_t d = 0, ph = 0, jph = 0;
+        for (int t = tile0; t < total; t += step) {
             const int m = t / a.tts * QW_ROWS + q * 32 + lane, n0 = t % a.tts * a.tok;
             const int cnt = min(min(a.tok, a.N - n0), most) - first; // tokens of this warp (any sign)
-            const __nv_bfloat16 *sp = a.s + min(m, a.M - 1);
+            const __nv_bfloat16 *sp = a.s + (size_t)gr0 * a.M + min(m, a.M - 1);
             float acc[48];
 #pragma unroll
             for (int c = 0; c < 48; ++c) acc[c] = 0.f;
@@ -1102,6 +1120,41 @@ __global__ void __launch_bounds__(QW_THREADS, 1)
                 }
             }
             if (!ok) break;
+            if (SPLIT) {
+                // all have read the last tile's
+                ok = mbar_wait_cl(jempty, jph ^ 1, limit, abort_flag, 532);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                const uint32_t to = smem_u32(join) + (uint32_t)(rank * a.own * QW_ROWS + q * 32 + lane) * 4;
+                int who = first / a.own, at = first - who * a.own; // block that finishes a token; its place there
+#pragma unroll
+                for (int c = 0; c < 48; ++c)
+                    if (c < cnt) {
+                        st_cluster_f32(mapa_shared(to + (uint32_t)at * (QW_ROWS * 4), who), acc[c]);
+                        if (++at == a.own) {
+                            at = 0;
+                            ++who;
+                        }
+                    }
+                fence_acq_rel_cluster();
+                __syncwarp();
+                if (lane < a.split) mbar_arrive_remote(mapa_shared(smem_u32(jfull), lane));
+                ok = mbar_wait_cl(jfull, jph, limit, abort_flag, 533);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                // this block's tokens, a warp every second one of its 32 rows
+                const int mine = min(a.own, min(a.tok, a.N - n0) - rank * a.own);
+                for (int c = warp >= 16; c < mine; c += 2) {
+                    const float *from = join + c * QW_ROWS + q * 32 + lane;
+                    float v = from[0];
+                    for (int r = 1; r < a.split; ++r) v += from[r * a.own * QW_ROWS];
+                    if (m < a.M) a.y[(size_t)(n0 + rank * a.own + c) * a.M + m] = __float2bfloat16_rn(v);
+                }
+                __syncwarp();
+                if (lane < a.split) mbar_arrive_remote(mapa_shared(smem_u32(jempty), lane));
+                jph ^= 1;
+                continue;
+            }
             if (m < a.M) {
                 __nv_bfloat16 *y = a.y + (size_t)(n0 + first) * a.M + m;
 #pragma unroll
@@ -1116,6 +1169,10 @@ __global__ void __launch_bounds__(QW_THREADS, 1)
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem_base, 512);
+    }
+    if (SPLIT) {
+        __syncwarp();
+        cluster_sync_all(); // no block leaves while another may still write to it
     }
 }
 

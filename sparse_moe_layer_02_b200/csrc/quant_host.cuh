@@ -112,22 +112,76 @@ int linear_quant_t(const void *q, const void *s, QuantArgs a, DeviceInfo *info, 
     return launch_quant<QUANT_LINEAR, RG, MT, KW, NT>(mW, mS, mW, mS, a, tiles, info, st);
 }
 
-template <int G>
-int launch_quant_wide(const CUtensorMap &mC, const CUtensorMap &mX, const QuantWideArgs &a, int grid,
-                      cudaStream_t st) {
-    static bool attr_set[kMaxDevices] = {}; // function attributes are set per device
-    const int dev = current_device_index();
-    if (dev < 0) return MOE_ERR_CUDA;
-    {
-        std::lock_guard<std::mutex> lk(g_mu);
-        if (!attr_set[dev]) {
-            if (cudaFuncSetAttribute(quant_wide_kernel<G>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     QW_SMEM) != cudaSuccess)
-                return MOE_ERR_CUDA;
-            attr_set[dev] = true;
+// Blocks that share a tile of the wide product: its time is that of the tiles one after the
+// other, each its share of the stages (0.6 us each with groups of 128) and what filling the
+// pipeline and joining the sums take, about six stages' time with a cluster and one without
+// (3 rounds of shares by 4 took 35 us where one round unshared took 29.5: 12288 x 5120, 24
+// tokens; 2816 x 4096, 22 row tiles on 148 SMs, took 11.4 shared by 6 and 23.7 unshared).
+struct WideSplit {
+    int split, grid;
+};
+WideSplit quant_wide_split(const int (&clusters)[9], size_t tiles, int stages) {
+    WideSplit best = {1, (int)std::min<size_t>(tiles, clusters[1])};
+    size_t least = SIZE_MAX;
+    for (int c = 1; c <= 8; ++c) {
+        if (clusters[c] <= 0 || stages < 2 * c) continue;
+        const size_t n = std::min<size_t>(tiles, clusters[c]);
+        const size_t time = ((tiles + n - 1) / n) * ((stages + c - 1) / c + (c > 1 ? 6 : 1));
+        if (time < least) {
+            least = time;
+            best = {c, (int)n * c};
         }
     }
-    return launch_serial(quant_wide_kernel<G>, dim3(grid, 1, 1), QW_THREADS, QW_SMEM, st, mC, mX, a);
+    return best;
+}
+
+template <int G>
+int launch_quant_wide(const CUtensorMap &mC, const CUtensorMap &mX, QuantWideArgs a, DeviceInfo *info,
+                      cudaStream_t st) {
+    static int clusters[kMaxDevices][9] = {}; // of 1 to 8 blocks that run at once; found once per device
+    const int dev = current_device_index();
+    if (dev < 0) return MOE_ERR_CUDA;
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(QW_THREADS, 1, 1);
+    cfg.dynamicSmemBytes = QW_SMEM;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    {
+        std::lock_guard<std::mutex> lk(g_mu);
+        if (!clusters[dev][1]) {
+            for (auto kernel : {quant_wide_kernel<G, false>, quant_wide_kernel<G, true>})
+                if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, QW_SMEM) !=
+                    cudaSuccess)
+                    return MOE_ERR_CUDA;
+            cfg.numAttrs = 1;
+            for (int c = 2; c <= 8; ++c) {
+                attr[0].val.clusterDim.x = c;
+                cfg.gridDim = dim3(info->sms / c * c, 1, 1);
+                if (cudaOccupancyMaxActiveClusters(&clusters[dev][c], quant_wide_kernel<G, true>, &cfg) !=
+                    cudaSuccess) {
+                    clusters[dev][c] = 0;
+                    cudaGetLastError();
+                }
+            }
+            clusters[dev][1] = info->sms;
+        }
+    }
+    const WideSplit w = quant_wide_split(clusters[dev], (size_t)a.nb * a.tts, (a.K + QW_COLS - 1) / QW_COLS);
+    a.split = w.split;
+    a.own = (a.tok + w.split - 1) / w.split;
+    attr[0].val.clusterDim.x = w.split;
+    cfg.gridDim = dim3(w.grid, 1, 1);
+    cfg.numAttrs = 2;
+    if (launch_ex(cfg, w.split > 1 ? quant_wide_kernel<G, true> : quant_wide_kernel<G, false>, mC, mX, a) !=
+        cudaSuccess)
+        return MOE_ERR_CUDA;
+    return launch_status();
 }
 
 // y = x w^T for more than 16 tokens.
@@ -158,11 +212,10 @@ int linear_quant_wide(const void *x, const void *q, const void *s, int N, int M,
            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS ||
         !make_map(&mX, x, K, N, K, a.tok))
         return MOE_ERR_CUDA;
-    const int grid = (int)std::min<size_t>((size_t)a.nb * a.tts, (size_t)info->sms);
     switch (G) {
-    case 32: return launch_quant_wide<32>(mC, mX, a, grid, st);
-    case 64: return launch_quant_wide<64>(mC, mX, a, grid, st);
-    default: return launch_quant_wide<128>(mC, mX, a, grid, st);
+    case 32: return launch_quant_wide<32>(mC, mX, a, info, st);
+    case 64: return launch_quant_wide<64>(mC, mX, a, info, st);
+    default: return launch_quant_wide<128>(mC, mX, a, info, st);
     }
 }
 
@@ -175,10 +228,15 @@ struct QuantWs {
     bool direct;
 };
 
-// Tokens of a tile.  One token: every pair is its own tile, no dispatch.
+// Tokens of a tile.  Tiles of 8 leave room for more stages of codes, tiles of 16 read an
+// expert's codes once where its tokens are more than 8 (us for the layer, 8 / 16): D 4096,
+// 128 experts of 1408, k 8: 12 tokens 150 / 157, 32 215 / 224, 64 261 / 267, 96 308 / 305,
+// 128 369 / 340; D 4096, 40 of 1024, k 4: 32 tokens 87 / 101, 64 110 / 116, 96 150 / 142, 512
+// 501 / 403.  The shared expert's codes are read again by every tile of tokens: D 6144,
+// 256 of 2048, k 8, 128 tokens (four an expert) 1035 / 1016.  (Tiles of 32 leave one block an
+// SM and were slower everywhere: the first at 512 tokens 1182, against 893.)
 int quant_tile_tokens(int N, int k, int E) {
-    if (N <= 8) return 8;
-    return (size_t)N * k <= (size_t)8 * E ? 16 : 32;
+    return N <= 8 || (N <= 64 && (size_t)N * k <= (size_t)4 * E) ? 8 : 16;
 }
 
 bool plan_quant(int N, int D, int E, int d, int d_sh, int k, QuantWs &W) {
@@ -334,10 +392,15 @@ int moe_linear_quant(const void *x, const void *q, const void *scales, int N, in
     a.ncols = M;
     a.out = y;
     a.wait_limit_ns = g_wait_limit_ns;
-    if (N <= 8) {
-        return linear_quant_t<4, 2, 128, 1>(q, scales, a, dev, st);
-    }
-    if (N <= 16) return linear_quant_t<4, 2, 128, 2>(q, scales, a, dev, st);
+    // Tiles of 8 tokens, of 16, or the tcgen05 kernel (us).  8 tokens as 16: 2816 x 4096,
+    // groups of 64, 9.3 against 8.3; 12288 x 6144 21.7 against 19.6.  16 tokens by tcgen05:
+    // 12288 x 6144, groups of 128, 34.6 against 28.2; 24 tokens, groups of 64 in tiles of 16:
+    // 2816 x 4096 14.1 against 12.0, 6144 x 6144 28.6 against 28.3, 12288 x 5120 37.9 against
+    // 34.2; 64 tokens there 66.6 against 39.3.  Groups of 32 make four sums of a stage there:
+    // 24 tokens, 12288 x 5120, 61 against 44 in tiles of 16; 48 tokens 59 against 44; 64
+    // tokens 67 against 72.
+    if (N <= 8) return linear_quant_t<4, 2, 128, 1>(q, scales, a, dev, st);
+    if (N <= 16 || (group == 32 && N <= 48)) return linear_quant_t<4, 2, 128, 2>(q, scales, a, dev, st);
     return linear_quant_wide(x, q, scales, N, M, K, group, y, dev, st);
 }
 
@@ -429,20 +492,13 @@ int moe_forward_quant(const void *x, const void *gate_up, const void *gate_up_sc
     // rows 152 us against 171.  The tiles are estimated, as the routing is on the device.
     const size_t tt = std::max<size_t>(std::min<size_t>((size_t)N * k, E), (size_t)N * k / W.tile_rows) +
                       (N + W.tile_rows - 1) / W.tile_rows;
-    const bool few = tt * ((d_moe + 127) / 128) < (size_t)dev->sms * (W.tile_rows == 32 ? 2 : 4);
-    switch (W.tile_rows) {
-    case 8:
+    const bool few = tt * ((d_moe + 127) / 128) < (size_t)dev->sms * 4;
+    if (W.tile_rows == 8)
         rc = few ? quant_layer_t<4, 2, 128, 1>(w, a, x, ws, W, dev, prof, st)
                  : quant_layer_t<8, 2, 128, 1>(w, a, x, ws, W, dev, prof, st);
-        break;
-    case 16:
+    else
         rc = few ? quant_layer_t<4, 2, 128, 2>(w, a, x, ws, W, dev, prof, st)
                  : quant_layer_t<8, 2, 128, 2>(w, a, x, ws, W, dev, prof, st);
-        break;
-    default:
-        rc = few ? quant_layer_t<4, 2, 128, 4>(w, a, x, ws, W, dev, prof, st)
-                 : quant_layer_t<8, 2, 128, 4>(w, a, x, ws, W, dev, prof, st);
-    }
     if (rc != MOE_OK) return rc;
     rc = launch_serial(quant_combine_kernel, dim3(N, (D + 4 * QC_THREADS - 1) / (4 * QC_THREADS), 1), QC_THREADS, 0, st, a,
                        (const float *)(ws + W.slot), (const float *)(ws + W.osh), (const int32_t *)dp.pos_of,

@@ -437,3 +437,24 @@ def test_what_a_call_makes_is_memory_of_the_calls_stream():
     got = [_run(x, w, ids, tw, stream=other) for _ in range(4)]  # workspaces taken and given back there
     torch.cuda.synchronize()
     assert all(torch.equal(y, want) for y in got)
+
+
+# Columns shared by the blocks of a cluster, for one row tile and for more tiles than
+# clusters; columns that end inside a stage of 128; token counts that no share divides.
+@pytest.mark.parametrize("N,M,K,G", [(17, 264, 1024, 64), (96, 8, 896, 64), (33, 40, 8192, 128), (90, 1032, 2208, 32),
+                                     (20, 2816, 4096, 32), (200, 520, 1504, 32), (77, 12288, 2048, 64),
+                                     (40, 24576, 1024, 128), (81, 12288, 5120, 32)])
+def test_product_of_many_tokens_in_clusters(N, M, K, G):
+    g = _gen(N + M + K)
+    q, s = moe.moe_quantize(_randn(g, M, K, std=0.02), G)
+    x = _randn(g, N, K)
+    w = _values(q, s)
+    y = x.double() @ w.t()
+    tol = _product_tol(x, w, K, y)
+    first = moe.moe_linear_quant(x, q, s)
+    for _ in range(3):
+        got = moe.moe_linear_quant(x, q, s)
+        bad = ~((got.double() - y).abs() <= tol)
+        assert not bad.any(), (int(bad.sum()), bad.nonzero()[:4].tolist())
+        assert torch.equal(got, first)
+    assert moe.moe_device_status() == 0
