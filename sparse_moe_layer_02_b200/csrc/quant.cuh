@@ -375,9 +375,15 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<RG, MT, KW, NT, G>::BLOCKS)
         }
     }
     // Nothing above touches global memory; all that follows comes after the previous
-    // kernel of the stream.
-    grid_dep_wait();
-    grid_dep_launch_dependents();
+    // kernel of the stream.  Only DOWN, whose previous kernel is always the layer's GATE_UP,
+    // waits further on: GATE_UP writes the tokens that DOWN reads and nothing else, and it
+    // was complete up to its own previous kernel when it let DOWN start, so the tables
+    // and the first stages of the weights are fetched while GATE_UP's last blocks run
+    // (one token, D 4096, 128 experts of 1408: 30.6 to 29.0 us for the layer).
+    if (KIND != QUANT_DOWN) {
+        grid_dep_wait();
+        grid_dep_launch_dependents();
+    }
     int routed = 0;
     if (KIND != QUANT_LINEAR) {
         if (a.direct) {
@@ -407,12 +413,47 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<RG, MT, KW, NT, G>::BLOCKS)
     const int total = KIND == QUANT_LINEAR ? a.nb * tts : routed + a.nb_s * tts;
     constexpr int gps = SK / G; // groups of a stage
     const uint64_t limit = a.wait_limit_ns;
+    if (KIND == QUANT_DOWN && warp != 8) {
+        grid_dep_wait();
+        grid_dep_launch_dependents();
+    }
 
     if (warp == 8) {
         // ------------------------------ producer ------------------------------
         const uint32_t stage_bytes = C::W_BYTES + 2 * HALF * gps * 2;
         uint32_t it = 0, s = 0, ph = 0; // stages issued, ring place and its parity
         bool ok = true;
+        // Codes and scales of the tile's stage i to the ring's place s (one lane).
+        auto fetch_weights = [&](const QuantTile &c, int i, uint32_t s) {
+            const CUtensorMap *w = c.shared ? &mW_s : &mW, *sc = c.shared ? &mS_s : &mS;
+            // GATE_UP's halves are gate rows and the up rows of the same columns, a box
+            // each; otherwise the tile's rows are consecutive, one box
+            const int r0 = KIND == QUANT_GATE_UP ? c.nb * HALF : c.nb * R;
+            const int r1 = r0 + (c.shared ? a.ncols_s : a.ncols);
+            mbar_arrive_expect_tx(&full[s], stage_bytes);
+            uint8_t *dw = ring_w + s * C::W_BYTES;
+#pragma unroll
+            for (int b = 0; b < C::NBOX; ++b) {
+                const int kx = i * (SK / 2) + b * C::BOX;
+                tma_load_3d(w, &full[s], dw + b * R * C::BOX, kx, r0, c.e);
+                if (KIND == QUANT_GATE_UP) tma_load_3d(w, &full[s], dw + (b * R + HALF) * C::BOX, kx, r1, c.e);
+            }
+            uint8_t *ds = ring_s + s * 2 * C::S_HALF;
+            tma_load_3d(sc, &full[s], ds, r0, i * gps, c.e);
+            if (KIND == QUANT_GATE_UP) tma_load_3d(sc, &full[s], ds + C::S_HALF, r1, i * gps, c.e);
+        };
+        uint32_t ahead = 0; // stages whose weights are on their way before the tokens are there
+        if (KIND == QUANT_DOWN) {
+            for (int t = tile0; t < total && ahead < C::STAGES; t += step) {
+                QuantTile c;
+                if (!quant_tile<KIND, TT>(t, routed, a, s_tile, s_cnt, c)) continue;
+                const int stages = ((c.shared ? a.K_s : a.K) + SK - 1) / SK;
+                for (int i = stages * rank / split; i < stages * (rank + 1) / split && ahead < C::STAGES; ++i, ++ahead)
+                    if (lane == 0) fetch_weights(c, i, ahead);
+            }
+            __syncwarp();
+            grid_dep_wait();
+        }
         for (int t = tile0; t < total && ok; t += step) {
             QuantTile c;
             if (!quant_tile<KIND, TT>(t, routed, a, s_tile, s_cnt, c)) continue;
@@ -426,30 +467,12 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<RG, MT, KW, NT, G>::BLOCKS)
                 if (KIND == QUANT_GATE_UP && !c.shared) row = a.direct ? 0 : a.perm_tok[row];
                 src = base + (size_t)row * rb;
             }
-            const CUtensorMap *w = c.shared ? &mW_s : &mW, *sc = c.shared ? &mS_s : &mS;
-            // GATE_UP's halves are gate rows and the up rows of the same columns, a box
-            // each; otherwise the tile's rows are consecutive, one box
-            const int r0 = KIND == QUANT_GATE_UP ? c.nb * HALF : c.nb * R;
-            const int r1 = r0 + (c.shared ? a.ncols_s : a.ncols);
             const int stages = (K + SK - 1) / SK;
             for (int i = stages * rank / split; i < stages * (rank + 1) / split; ++i) {
                 if (lane == 0) ok = mbar_wait(&empty[s], ph ^ 1, limit, abort_flag, 401);
                 ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
                 if (!ok) break;
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(&full[s], stage_bytes);
-                    uint8_t *dw = ring_w + s * C::W_BYTES;
-#pragma unroll
-                    for (int b = 0; b < C::NBOX; ++b) {
-                        const int kx = i * (SK / 2) + b * C::BOX;
-                        tma_load_3d(w, &full[s], dw + b * R * C::BOX, kx, r0, c.e);
-                        if (KIND == QUANT_GATE_UP)
-                            tma_load_3d(w, &full[s], dw + (b * R + HALF) * C::BOX, kx, r1, c.e);
-                    }
-                    uint8_t *ds = ring_s + s * 2 * C::S_HALF;
-                    tma_load_3d(sc, &full[s], ds, r0, i * gps, c.e);
-                    if (KIND == QUANT_GATE_UP) tma_load_3d(sc, &full[s], ds + C::S_HALF, r1, i * gps, c.e);
-                }
+                if (lane == 0 && it >= ahead) fetch_weights(c, i, s);
                 fence_proxy_async_smem(); // the shaper wrote there before
                 const uint32_t bytes = (uint32_t)min(SK, K - i * SK) * 2;
                 if (lane == 0) mbar_arrive_expect_tx(&raw[s], bytes * c.cnt);
@@ -464,10 +487,10 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<RG, MT, KW, NT, G>::BLOCKS)
         }
         if (!ok && lane == 0) {
             // Let copies already issued land before the block's memory goes away.
-            const uint32_t first = it > C::STAGES ? it - C::STAGES : 0;
-            for (uint32_t j = first; j < it; ++j) {
+            const uint32_t last = it > ahead ? it : ahead;
+            for (uint32_t j = last > C::STAGES ? last - C::STAGES : 0; j < last; ++j) {
                 volatile int no_abort = 0;
-                mbar_wait(&raw[j % C::STAGES], (j / C::STAGES) & 1, 10000000ull, &no_abort, 402);
+                if (j < it) mbar_wait(&raw[j % C::STAGES], (j / C::STAGES) & 1, 10000000ull, &no_abort, 402);
                 mbar_wait(&full[j % C::STAGES], (j / C::STAGES) & 1, 10000000ull, &no_abort, 403);
             }
         }
