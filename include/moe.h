@@ -298,7 +298,8 @@ unsigned long long moe_launch_count(void);
  *   W, dW   [E, M, K]   dtype      offsets [E+1]       int32, device, 4-byte aligned
  * dtype MOE_BF16: tensor cores, fp32 accumulation, one rounding; M and K multiples
  * of 8.  MOE_F32: CUDA cores, fp32 sums in index order; M and K multiples of 4.
- * 1 <= E <= 512.  No workspace; results are bitwise reproducible.
+ * 1 <= E <= 512.  No workspace; results are bitwise reproducible (for the same
+ * sizes: how many blocks share a bf16 sum depends on them).
  * Rows of no expert (before offsets[0], from offsets[E] on) are not read; in y and
  * dx they are left as they were, or written zero if zero_rest is not 0.
  * Offsets are clamped to [0, rows] and to be non-decreasing; if that changes any,

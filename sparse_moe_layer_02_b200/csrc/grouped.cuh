@@ -63,6 +63,7 @@ struct GroupedArgs {
     int wide;     // MN-major operands: one load for all of a tile's 64-column boxes
     void *out;
     int zero_rest; // forward, dgrad: write zeros to the rows of no expert
+    int split;    // blocks of a cluster that share a tile's k-blocks
     uint64_t wait_limit_ns;
 };
 
@@ -93,6 +94,9 @@ __device__ __forceinline__ void tma_load_4d(const CUtensorMap *map, uint64_t *ba
         " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_u32(dst)),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
         : "memory");
+}
+__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 __device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, const void *src, int c0, int c1,
                                              int c2) {
@@ -197,7 +201,13 @@ __device__ __forceinline__ GroupedTile grouped_tile(int t, const GroupedArgs &a,
 // mOut y [rows, M] box 64 x 32.  dgrad: mA dy [rows, M] box 64 x 128, mB W box
 // 64 x 64 x 1, mOut dx [rows, K].  wgrad: mA dy box 64 x 64, mB x [rows, K] box
 // 64 x 64, mOut dW [E, M, K] box 64 x 32 x 1.
-template <int MODE>
+//
+// SPLIT, for few tiles with a long sum: the blocks of a cluster (2, 4 or 8) take a tile's
+// k-blocks in equal shares, one tile a cluster.  The accumulators are cut into 16 parts of
+// 32 rows x 64 columns; part p is finished by block p % split, which gets the others' sums
+// through distributed shared memory (over the ring, which is empty by then) and adds them
+// in the blocks' order.
+template <int MODE, bool SPLIT>
 __global__ void __launch_bounds__(GrpCfg<MODE>::THREADS, 1)
     grouped_product_kernel(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtensorMap mB,
                            const __grid_constant__ CUtensorMap mOut, const GroupedArgs a) {
@@ -247,19 +257,61 @@ __global__ void __launch_bounds__(GrpCfg<MODE>::THREADS, 1)
     const uint32_t tmem_base = *tmem_slot;
     const int total = MODE == GRP_WGRAD ? a.E * a.nb * a.mb : s_tile[a.E] * a.nb;
     const uint64_t limit = a.wait_limit_ns;
+    const int split = SPLIT ? a.split : 1, rank = SPLIT ? (int)cluster_ctarank() : 0;
+    const int tile0 = blockIdx.x / split, step = gridDim.x / split;
+
+    // An epilogue warp stores 32 rows (32 q ...) x 64 columns (64 ch ...) of a tile, a lane's
+    // row in v.  wgrad's rows past M are clipped by the store's map; in the other modes a
+    // part of 32 rows inside the segment is stored by TMA, a ragged one by each row's thread.
+    auto emit = [&](const GroupedTile &c, int q, int ch, const uint32_t (&v)[2][32]) {
+        uint8_t *stg = smem + C::STG_OFF + (warp - 2) * GRP_OUT_BUF + lane * 128; // this lane's row
+        const int first = q * 32, col = c.n0 + ch * 64;
+        const int rows = (MODE == GRP_WGRAD ? a.M - c.m0 : c.r1 - c.r0) - first;
+        uint4 u[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const uint32_t *f = &v[j / 4][(j % 4) * 8];
+            u[j] = make_uint4(pack_bf16x2(__uint_as_float(f[0]), __uint_as_float(f[1])),
+                              pack_bf16x2(__uint_as_float(f[2]), __uint_as_float(f[3])),
+                              pack_bf16x2(__uint_as_float(f[4]), __uint_as_float(f[5])),
+                              pack_bf16x2(__uint_as_float(f[6]), __uint_as_float(f[7])));
+        }
+        if (MODE == GRP_WGRAD || rows >= 32) {
+            if (lane == 0) bulk_wait_group_read<0>(); // the last box has left the buffer
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < 8; ++j) // at the places of the 128-byte swizzle
+                *reinterpret_cast<uint4 *>(stg + ((j ^ (lane & 7)) << 4)) = u[j];
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                if (MODE == GRP_WGRAD)
+                    tma_store_3d(&mOut, stg, col, c.m0 + first, c.e);
+                else
+                    tma_store_2d(&mOut, stg, col, c.r0 + first);
+                bulk_commit_group();
+            }
+        } else if (lane < rows) {
+            uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) +
+                                                   (size_t)(c.r0 + first + lane) * a.ncols + col);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (col + 8 * j < a.ncols) dst[j] = u[j];
+        }
+    };
 
     if (warp == 0) {
         // ------------------------------ TMA producer ------------------------------
         if (lane == 0) {
             uint32_t it = 0;
             bool ok = true;
-            for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+            for (int t = tile0; t < total && ok; t += step) {
                 const GroupedTile c = grouped_tile<MODE>(t, a, s_off, s_tile);
                 // Column blocks of one row tile start at different k-blocks, so they do
                 // not all ask for the same rows at once.  (wgrad keeps the order: its
                 // last k-block is the one that is cut.)
-                const int rot = MODE == GRP_WGRAD ? 0 : (c.n0 / GRP_BN) % c.kb;
-                for (int i = 0; i < c.kb; ++i, ++it) {
+                const int rot = MODE == GRP_WGRAD || SPLIT ? 0 : (c.n0 / GRP_BN) % c.kb;
+                for (int i = c.kb * rank / split; i < c.kb * (rank + 1) / split; ++i, ++it) {
                     const int kb = i + rot < c.kb ? i + rot : i + rot - c.kb;
                     const uint32_t s = it % GRP_STAGES, ph = (it / GRP_STAGES) & 1;
                     if (!mbar_wait(&empty[s], ph ^ 1, limit, abort_flag, 301)) { ok = false; break; }
@@ -307,9 +359,10 @@ __global__ void __launch_bounds__(GrpCfg<MODE>::THREADS, 1)
         // lane 0 waits and issues.
         uint32_t it = 0, tc = 0;
         bool ok = true;
-        for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+        for (int t = tile0; t < total && ok; t += step) {
             const GroupedTile c = grouped_tile<MODE>(t, a, s_off, s_tile);
-            if (c.kb == 0) continue; // wgrad of an expert without rows: zeros
+            const int i0 = c.kb * rank / split, i1 = c.kb * (rank + 1) / split;
+            if (i0 == i1) continue; // wgrad of an expert without rows (or with few): zeros
             const uint32_t acc = tc & 1, aph = (tc >> 1) & 1;
             ++tc;
             // only the columns that exist, in steps of 16
@@ -321,7 +374,7 @@ __global__ void __launch_bounds__(GrpCfg<MODE>::THREADS, 1)
             if (!ok) break;
             tc_fence_after();
             const uint32_t d_tmem = tmem_base + acc * GRP_BN;
-            for (int i = 0; i < c.kb; ++i, ++it) {
+            for (int i = i0; i < i1; ++i, ++it) {
                 const uint32_t s = it % GRP_STAGES, ph = (it / GRP_STAGES) & 1;
                 if (lane == 0) ok = mbar_wait(&full[s], ph, limit, abort_flag, 312);
                 ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
@@ -354,7 +407,7 @@ __global__ void __launch_bounds__(GrpCfg<MODE>::THREADS, 1)
                         const uint64_t db = MODE != GRP_FORWARD
                                                 ? umma_desc_sw128_mn(sb + kk * 2048, GRP_CHUNK)
                                                 : umma_desc_sw128(sb + kk * 32);
-                        umma_bf16_ss(d_tmem, da, db, idesc, (i > 0 || kk > 0) ? 1u : 0u);
+                        umma_bf16_ss(d_tmem, da, db, idesc, (i > i0 || kk > 0) ? 1u : 0u);
                     }
                     umma_commit(&empty[s]);
                 }
@@ -369,13 +422,18 @@ __global__ void __launch_bounds__(GrpCfg<MODE>::THREADS, 1)
             mbar_wait(drain, 0, 100000000ull, &no_abort, 313);
         }
         __syncwarp();
+    } else if (SPLIT) {
+        if (tile0 < total && lane == 0) {
+            const GroupedTile c = grouped_tile<MODE>(tile0, a, s_off, s_tile);
+            if (c.kb * rank / split < c.kb * (rank + 1) / split) mbar_wait(&tfull[0], 0, limit, abort_flag, 321);
+        }
+        __syncwarp();
     } else {
         // ------------------------------ epilogue ---------------------------------
         const int q = warp & 3; // TMEM lane quadrant: output rows q*32 + lane of the tile
         const int part = (warp - 2) >> 2; // of the tile's columns
-        uint8_t *stg = smem + C::STG_OFF + (warp - 2) * GRP_OUT_BUF + lane * 128; // this lane's row
         uint32_t tc = 0;
-        for (int t = blockIdx.x; t < total; t += gridDim.x) {
+        for (int t = tile0; t < total; t += step) {
             const GroupedTile c = grouped_tile<MODE>(t, a, s_off, s_tile);
             const bool none = c.kb == 0; // nothing accumulated: zeros
             const uint32_t acc = tc & 1, aph = (tc >> 1) & 1;
@@ -401,12 +459,9 @@ __global__ void __launch_bounds__(GrpCfg<MODE>::THREADS, 1)
                             make_uint4(0u, 0u, 0u, 0u);
                 continue;
             }
-            // wgrad's rows past M are clipped by the store's map; in the other modes a part
-            // of 32 rows inside the segment is stored by TMA, a ragged one by each row's
-            // thread.  64 columns at a time: while one box is read from shared memory, the
-            // next columns come from TMEM (boxes of 32 columns, two in turn: 1300 cycles
-            // each, more than the MMAs of a short tile).
-            const bool by_tma = MODE == GRP_WGRAD || rows >= 32;
+            // 64 columns at a time: while one box is read from shared memory, the next
+            // columns come from TMEM (boxes of 32 columns, two in turn: 1300 cycles each,
+            // more than the MMAs of a short tile).
 #pragma unroll 1
             for (int ch = part * C::COLS / 64; ch < (part + 1) * C::COLS / 64; ++ch) {
                 const int col = c.n0 + ch * 64;
@@ -415,43 +470,63 @@ __global__ void __launch_bounds__(GrpCfg<MODE>::THREADS, 1)
                 tmem_ld_32x32b_x32(tbase + ch * 64, v[0]);
                 tmem_ld_32x32b_x32(tbase + ch * 64 + 32, v[1]);
                 tmem_ld_wait();
-                uint4 u[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const uint32_t *f = &v[j / 4][(j % 4) * 8];
-                    u[j] = make_uint4(pack_bf16x2(__uint_as_float(f[0]), __uint_as_float(f[1])),
-                                      pack_bf16x2(__uint_as_float(f[2]), __uint_as_float(f[3])),
-                                      pack_bf16x2(__uint_as_float(f[4]), __uint_as_float(f[5])),
-                                      pack_bf16x2(__uint_as_float(f[6]), __uint_as_float(f[7])));
-                }
-                if (by_tma) {
-                    if (lane == 0) bulk_wait_group_read<0>(); // the last box has left the buffer
-                    __syncwarp();
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) // at the places of the 128-byte swizzle
-                        *reinterpret_cast<uint4 *>(stg + ((j ^ (lane & 7)) << 4)) = u[j];
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) {
-                        if (MODE == GRP_WGRAD)
-                            tma_store_3d(&mOut, stg, col, c.m0 + first, c.e);
-                        else
-                            tma_store_2d(&mOut, stg, col, c.r0 + first);
-                        bulk_commit_group();
-                    }
-                } else if (lane < rows) {
-                    uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) +
-                                                           (size_t)(c.r0 + first + lane) * a.ncols + col);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        if (col + 8 * j < a.ncols) dst[j] = u[j];
-                }
+                emit(c, q, ch, v);
             }
             // Release the accumulator.
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&tempty[acc]);
         }
+    }
+    if (SPLIT) {
+        __syncwarp();
+        cluster_sync_all(); // every block's ring has been read
+        if (warp >= 2 && tile0 < total) {
+            const GroupedTile c = grouped_tile<MODE>(tile0, a, s_off, s_tile);
+            const int q = warp & 3, rows = (MODE == GRP_WGRAD ? a.M - c.m0 : c.r1 - c.r0) - q * 32;
+            const int part = (warp - 2) >> 2;
+            tc_fence_after();
+            if (c.kb * rank / split < c.kb * (rank + 1) / split && rows > 0) {
+#pragma unroll 1
+                for (int ch = part * C::COLS / 64; ch < (part + 1) * C::COLS / 64; ++ch) {
+                    if (c.n0 + ch * 64 >= a.ncols) break;
+                    uint32_t v[2][32];
+                    const uint32_t from = tmem_base + ((uint32_t)(q * 32) << 16) + ch * 64;
+                    tmem_ld_32x32b_x32(from, v[0]);
+                    tmem_ld_32x32b_x32(from + 32, v[1]);
+                    tmem_ld_wait();
+                    // [own part][block][column][row]
+                    const int p = q * 4 + ch;
+                    const uint32_t to = mapa_shared(
+                        smem_u32(ring) + (uint32_t)(((p / split) * split + rank) * 64 * 32 + lane) * 4, p % split);
+#pragma unroll
+                    for (int j = 0; j < 64; ++j) st_cluster_f32(to + j * 128, __uint_as_float(v[j / 32][j % 32]));
+                }
+            }
+        }
+        __syncwarp();
+        cluster_sync_all(); // all sums are there
+        if (warp >= 2 && tile0 < total) {
+            const GroupedTile c = grouped_tile<MODE>(tile0, a, s_off, s_tile);
+            for (int own = warp - 2; own < 16 / split; own += C::EPI) {
+                const int p = own * split + rank, q = p / 4, ch = p % 4;
+                const int rows = (MODE == GRP_WGRAD ? a.M - c.m0 : c.r1 - c.r0) - q * 32;
+                if (c.n0 + ch * 64 >= a.ncols || rows <= 0) continue;
+                uint32_t v[2][32];
+#pragma unroll
+                for (int j = 0; j < 64; ++j) v[j / 32][j % 32] = 0;
+                for (int r = 0; r < split; ++r) {
+                    if (c.kb * r / split == c.kb * (r + 1) / split) continue; // nothing summed there
+                    const float *from = reinterpret_cast<const float *>(ring) + (own * split + r) * 64 * 32 + lane;
+#pragma unroll
+                    for (int j = 0; j < 64; ++j)
+                        v[j / 32][j % 32] = __float_as_uint(__uint_as_float(v[j / 32][j % 32]) + from[j * 32]);
+                }
+                emit(c, q, ch, v);
+            }
+        }
+    }
+    if (warp >= 2) {
         if (lane == 0) bulk_wait_group<0>(); // stores done
         if (MODE != GRP_WGRAD && a.zero_rest)
             grouped_zero_rest(a.out, a.rows, (size_t)a.ncols * 2, s_off[0], s_off[a.E],

@@ -56,24 +56,81 @@ int launch_serial(void (*kernel)(KArgs...), dim3 grid, int threads, int smem, cu
     return launch_status();
 }
 
+// Clusters of n blocks of a kernel that run at once, 0 where they cannot.
+template <typename... KArgs>
+int clusters_at_once(void (*kernel)(KArgs...), int n, int threads, int smem, int sms) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(sms / n * n, 1, 1);
+    cfg.blockDim = dim3(threads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = n;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int count = 0;
+    if (cudaOccupancyMaxActiveClusters(&count, kernel, &cfg) == cudaSuccess) return count;
+    cudaGetLastError();
+    return 0;
+}
+
+// Launch with clusters of `split` blocks, and with programmatic serialization as above.
+template <typename... KArgs, typename... Args>
+int launch_clusters(void (*kernel)(KArgs...), int split, int grid, int threads, int smem, cudaStream_t st,
+                    Args &&...args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid, 1, 1);
+    cfg.blockDim = dim3(threads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = split;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    if (launch_ex(cfg, kernel, args...) != cudaSuccess) return MOE_ERR_CUDA;
+    return launch_status();
+}
+
+// kb: a tile's k-blocks (wgrad: on average).
 template <int MODE>
 int launch_grouped(const CUtensorMap &mA, const CUtensorMap &mB, const CUtensorMap &mOut,
-                   const GroupedArgs &a, int grid, cudaStream_t st) {
-    static bool attr_set[kMaxDevices] = {}; // function attributes are set per device
+                   GroupedArgs a, size_t tiles, int kb, DeviceInfo *info, cudaStream_t st) {
+    using C = GrpCfg<MODE>;
+    static int clusters[kMaxDevices][4] = {}; // of 1, 2, 4, 8 blocks at once; found once per device
     const int dev = current_device_index();
     if (dev < 0) return MOE_ERR_CUDA;
     {
         std::lock_guard<std::mutex> lk(g_mu);
-        if (!attr_set[dev]) {
-            if (cudaFuncSetAttribute(grouped_product_kernel<MODE>,
-                                     cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     GrpCfg<MODE>::SMEM) != cudaSuccess)
-                return MOE_ERR_CUDA;
-            attr_set[dev] = true;
+        if (!clusters[dev][0]) {
+            for (auto kernel : {grouped_product_kernel<MODE, false>, grouped_product_kernel<MODE, true>})
+                if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) !=
+                    cudaSuccess)
+                    return MOE_ERR_CUDA;
+            for (int i = 1; i < 4; ++i)
+                clusters[dev][i] = clusters_at_once(grouped_product_kernel<MODE, true>, 1 << i, C::THREADS, C::SMEM,
+                                                    info->sms);
+            clusters[dev][0] = info->sms;
         }
     }
-    return launch_serial(grouped_product_kernel<MODE>, dim3(grid, 1, 1), GrpCfg<MODE>::THREADS,
-                         GrpCfg<MODE>::SMEM, st, mA, mB, mOut, a);
+    // As many blocks share a tile as leave each tile a cluster of its own, at once, and each
+    // block 8 k-blocks: joining costs 2 to 3 us (us, unshared / shared): forward, 1 row,
+    // 1024 x 6144 37.5 / 13.9, 64 rows, 6144 x 6144 38.8 / 19.0; wgrad, 65536 rows, 512 x 512
+    // 454 / 72.  With shares of 4: forward, 4096 rows, 4 x 512 x 512 9.1 / 12.0.
+    a.split = 1;
+    for (int i = 1; i < 4; ++i)
+        if (tiles <= (size_t)clusters[dev][i] && kb >= 8 << i) a.split = 1 << i;
+    if (a.split > 1)
+        return launch_clusters(grouped_product_kernel<MODE, true>, a.split, (int)tiles * a.split, C::THREADS, C::SMEM,
+                               st, mA, mB, mOut, a);
+    return launch_serial(grouped_product_kernel<MODE, false>, dim3((unsigned)std::min<size_t>(tiles, info->sms), 1, 1),
+                         C::THREADS, C::SMEM, st, mA, mB, mOut, a);
 }
 
 // One product.  A and B: forward x, W; dgrad dy, W; wgrad dy, x.
@@ -159,8 +216,8 @@ int grouped_impl(const void *A, const void *B, const int32_t *offsets, int rows,
     if (!ok) return MOE_ERR_CUDA;
     const size_t tiles = MODE == GRP_WGRAD ? (size_t)E * a.nb * a.mb
                                            : ((size_t)rows / GRP_BM + std::min(rows, E)) * a.nb;
-    const int grid = (int)std::min<size_t>(tiles, (size_t)dev->sms);
-    return launch_grouped<MODE>(mA, mB, mOut, a, grid, st);
+    const int kb = (int)((MODE == GRP_WGRAD ? (size_t)rows / E : (size_t)a.red) / GRP_BK);
+    return launch_grouped<MODE>(mA, mB, mOut, a, tiles, kb, dev, st);
 }
 
 }  // namespace

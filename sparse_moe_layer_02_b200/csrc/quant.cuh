@@ -284,9 +284,6 @@ __device__ __forceinline__ bool quant_tile(int t, int routed, const QuantArgs &a
     return true;
 }
 
-__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
-    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
-}
 __device__ __forceinline__ void fence_acq_rel_cluster() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
 
 // Bulk copy of consecutive bytes into shared memory (16-byte aligned, a multiple of 16).

@@ -72,23 +72,9 @@ int launch_quant_g(const CUtensorMap &mW, const CUtensorMap &mS, const CUtensorM
     const size_t slots = (size_t)info->sms * C::BLOCKS;
     QuantArgs b = a;
     b.split = C::KS > 1 ? quant_split(tiles, slots, (std::max(a.K, a.K_s) + C::SK - 1) / C::SK) : 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(std::min<size_t>(tiles, slots / b.split) * b.split), 1, 1);
-    cfg.blockDim = dim3(QM_THREADS, 1, 1);
-    cfg.dynamicSmemBytes = C::SMEM;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = b.split;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[1].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    if (launch_ex(cfg, quant_product_kernel<KIND, RG, MT, KW, NT, G>, mW, mS, mW_s, mS_s, b) != cudaSuccess)
-        return MOE_ERR_CUDA;
-    return launch_status();
+    return launch_clusters(quant_product_kernel<KIND, RG, MT, KW, NT, G>, b.split,
+                           (int)(std::min<size_t>(tiles, slots / b.split) * b.split), QM_THREADS, C::SMEM, st, mW, mS,
+                           mW_s, mS_s, b);
 }
 
 template <int KIND, int RG, int MT, int KW, int NT>
@@ -141,17 +127,6 @@ int launch_quant_wide(const CUtensorMap &mC, const CUtensorMap &mX, QuantWideArg
     static int clusters[kMaxDevices][9] = {}; // of 1 to 8 blocks that run at once; found once per device
     const int dev = current_device_index();
     if (dev < 0) return MOE_ERR_CUDA;
-    cudaLaunchConfig_t cfg = {};
-    cfg.blockDim = dim3(QW_THREADS, 1, 1);
-    cfg.dynamicSmemBytes = QW_SMEM;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[1].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
     {
         std::lock_guard<std::mutex> lk(g_mu);
         if (!clusters[dev][1]) {
@@ -159,29 +134,16 @@ int launch_quant_wide(const CUtensorMap &mC, const CUtensorMap &mX, QuantWideArg
                 if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, QW_SMEM) !=
                     cudaSuccess)
                     return MOE_ERR_CUDA;
-            cfg.numAttrs = 1;
-            for (int c = 2; c <= 8; ++c) {
-                attr[0].val.clusterDim.x = c;
-                cfg.gridDim = dim3(info->sms / c * c, 1, 1);
-                if (cudaOccupancyMaxActiveClusters(&clusters[dev][c], quant_wide_kernel<G, true>, &cfg) !=
-                    cudaSuccess) {
-                    clusters[dev][c] = 0;
-                    cudaGetLastError();
-                }
-            }
+            for (int c = 2; c <= 8; ++c)
+                clusters[dev][c] = clusters_at_once(quant_wide_kernel<G, true>, c, QW_THREADS, QW_SMEM, info->sms);
             clusters[dev][1] = info->sms;
         }
     }
     const WideSplit w = quant_wide_split(clusters[dev], (size_t)a.nb * a.tts, (a.K + QW_COLS - 1) / QW_COLS);
     a.split = w.split;
     a.own = (a.tok + w.split - 1) / w.split;
-    attr[0].val.clusterDim.x = w.split;
-    cfg.gridDim = dim3(w.grid, 1, 1);
-    cfg.numAttrs = 2;
-    if (launch_ex(cfg, w.split > 1 ? quant_wide_kernel<G, true> : quant_wide_kernel<G, false>, mC, mX, a) !=
-        cudaSuccess)
-        return MOE_ERR_CUDA;
-    return launch_status();
+    return launch_clusters(w.split > 1 ? quant_wide_kernel<G, true> : quant_wide_kernel<G, false>, w.split, w.grid,
+                           QW_THREADS, QW_SMEM, st, mC, mX, a);
 }
 
 // y = x w^T for more than 16 tokens.

@@ -274,7 +274,16 @@ def test_an_output_with_gradients_is_refused():
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
 def test_offsets_past_32_bits(dtype):
-    """More than 2^31 elements of x, and of W: the last rows and the last expert are right."""
+    """More than 2^31 elements of x, and of W: the last rows and the last expert are right.
+
+    fp32 sums are in index order whatever the sizes: equal to those of a small call.  How many
+    blocks share a bf16 sum depends on the number of tiles, so those are held to fp64, with
+    the bound above and 2 * 2^-22 for the 7 additions of 2^-24 that join 8 shares."""
+    def same(got, small, exact, mass, n):
+        if dtype == F32:
+            assert torch.equal(got, small())
+        else:
+            _check(got, exact, mass, n + 32, BF16)
     K, M, rows = 4096, 8, 2 ** 31 // 4096 + 700
     g = torch.Generator(device=DEV)
     g.manual_seed(0)
@@ -284,15 +293,16 @@ def test_offsets_past_32_bits(dtype):
     dy = torch.ones((rows, M), dtype=dtype, device=DEV)
     off = torch.tensor([0, rows - 333, rows], dtype=torch.int32, device=DEV)
     xs, small = x[-500:].clone(), torch.tensor([0, 167, 500], dtype=torch.int32, device=DEV)
+    (ye, ym), (dxe, dxm), (dWe, dWm) = _oracle(xs, W, dy[-500:], small)
     y = moe.moe_grouped_linear(x, W, off)
-    assert torch.equal(y[-500:], moe.moe_grouped_linear(xs, W, small))
+    same(y[-500:], lambda: moe.moe_grouped_linear(xs, W, small), ye, ym, K)
     assert (y[:-500] == 0).all()
     del y
     dx = moe.moe_grouped_linear_dgrad(dy, W, off)
-    assert torch.equal(dx[-500:], moe.moe_grouped_linear_dgrad(dy[-500:], W, small))
+    same(dx[-500:], lambda: moe.moe_grouped_linear_dgrad(dy[-500:], W, small), dxe, dxm, M)
     del dx
     dW = moe.moe_grouped_linear_wgrad(dy, x, off)
-    assert torch.equal(dW[1], moe.moe_grouped_linear_wgrad(dy[-500:], xs, small)[1])
+    same(dW[1], lambda: moe.moe_grouped_linear_wgrad(dy[-500:], xs, small)[1], dWe[1], dWm[1], 333)
     del x, W, dy, dW
     E = 2 ** 31 // (1056 * 4096) + 1  # 497, of at most 512
     W = torch.zeros((E, 1056, 4096), dtype=dtype, device=DEV)
@@ -300,11 +310,13 @@ def test_offsets_past_32_bits(dtype):
     off = torch.zeros(E + 1, dtype=torch.int32, device=DEV)
     off[-1] = 500
     one = torch.tensor([0, 500], dtype=torch.int32, device=DEV)
-    assert torch.equal(moe.moe_grouped_linear(xs, W, off), moe.moe_grouped_linear(xs, W[-1:], one))
     dy = torch.randn((500, 1056), generator=g, device=DEV).to(dtype)
-    assert torch.equal(moe.moe_grouped_linear_dgrad(dy, W, off), moe.moe_grouped_linear_dgrad(dy, W[-1:], one))
+    (ye, ym), (dxe, dxm), (dWe, dWm) = _oracle(xs, W[-1:], dy, one)
+    same(moe.moe_grouped_linear(xs, W, off), lambda: moe.moe_grouped_linear(xs, W[-1:], one), ye, ym, 4096)
+    same(moe.moe_grouped_linear_dgrad(dy, W, off), lambda: moe.moe_grouped_linear_dgrad(dy, W[-1:], one), dxe, dxm, 1056)
     dW = moe.moe_grouped_linear_wgrad(dy, xs, off, dW=W)
-    assert torch.equal(dW[-1], moe.moe_grouped_linear_wgrad(dy, xs, one)[0]) and (dW[:-1] == 0).all()
+    same(dW[-1], lambda: moe.moe_grouped_linear_wgrad(dy, xs, one)[0], dWe[0], dWm[0], 500)
+    assert (dW[:-1] == 0).all()
     assert moe.moe_device_status() == 0
 
 
@@ -357,3 +369,44 @@ def test_what_a_call_makes_is_memory_of_the_calls_stream():
         got = f(stream=other)
         torch.cuda.synchronize()
         assert torch.equal(got, want)
+
+
+# Few tiles with long sums: the k-blocks of a tile are shared by 2, 4 or 8 blocks, whose
+# sums are added in fp32 (7 roundings of 2^-24 at most: two more steps of 2^-22, or 32 more
+# products to _check).  Shares that differ, experts with no rows or too few for a share.
+@pytest.mark.parametrize("sizes,M,K,lead,spare", [
+    ([5], 264, 4104, 0, 0), ([130, 0, 3], 2056, 136, 3, 2), ([1700, 0, 2100], 200, 72, 0, 50),
+    ([9001], 136, 520, 7, 0), ([40, 2000, 1, 70, 63, 0, 64, 65], 128, 264, 0, 0), ([33], 4096, 2048, 0, 0),
+    ([600, 601], 1024, 1536, 0, 0),
+    ([3000, 40, 0, 4500, 100], 200, 136, 0, 9)])
+def test_products_of_few_tiles_match_fp64(sizes, M, K, lead, spare):
+    x, W, dy, off = _case(sizes, M, K, BF16, lead, spare)
+    (y, ym), (dx, dxm), (dW, dWm) = _oracle(x, W, dy, off)
+    rest = torch.ones(x.shape[0], dtype=torch.bool, device=DEV)
+    rest[lead:lead + sum(sizes)] = False
+    x[rest], dy[rest] = float("nan"), float("inf")
+    calls = (lambda: moe.moe_grouped_linear(x, W, off), lambda: moe.moe_grouped_linear_dgrad(dy, W, off),
+             lambda: moe.moe_grouped_linear_wgrad(dy, x, off))
+    for f, t, m, n in zip(calls, (y, dx, dW), (ym, dxm, dWm), (K, M, max(sizes))):
+        got = f()
+        _check(got, t, m, n + 32, BF16)
+        assert all(torch.equal(f(), got) for _ in range(3))
+    assert moe.moe_device_status() == 0
+    y = moe.moe_grouped_linear(x, W, off, y=torch.full_like(dy, 7.0))
+    assert (y[rest] == 7.0).all()
+
+
+def test_a_wait_that_runs_out_among_few_tiles_leaves_the_device_usable():
+    x, W, dy, off = _case([2000, 40], 128, 2048, BF16)
+    calls = (lambda: moe.moe_grouped_linear(x, W, off), lambda: moe.moe_grouped_linear_wgrad(dy, x, off))
+    want = [f() for f in calls]
+    torch.cuda.synchronize()
+    moe.moe_debug_set_wait_limit_ns(1)
+    try:
+        for f in calls:
+            f()
+            assert moe.moe_device_status() in (0, -6)
+    finally:
+        moe.moe_debug_set_wait_limit_ns(0)
+    assert all(torch.equal(f(), w) for f, w in zip(calls, want))
+    assert moe.moe_device_status() == 0
