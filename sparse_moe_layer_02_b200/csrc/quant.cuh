@@ -781,7 +781,7 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<RG, MT, KW, NT, G>::BLOCKS)
 }
 
 // ---------------------------------------------------------------------------
-// The product of one matrix with more than 16 tokens.  There the register kernel's MMA
+// The product of one matrix with more than 16 tokens (48 with groups of 32).  There the register kernel's MMA
 // time grows with the tokens (mma.sync m16n8k16, 8 cycles each), so tcgen05 takes over:
 // a tile is 128 weight rows x up to 96 tokens, one block per SM.  Where that leaves SMs
 // idle, the blocks of a cluster share a tile's columns: each sums its own, hands every
@@ -801,11 +801,12 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<RG, MT, KW, NT, G>::BLOCKS)
 //                thread = row; sum += scale * group, in fp32 registers
 //
 // The weights are not rounded: integers times tokens are exact in the MMA's fp32 and the
-// scale is applied once per group outside.  A K = 16 MMA takes 45 cycles or more however
-// few the tokens (64 at 128), so a tile of 128 columns takes 400-500 cycles, about what
-// its codes take from memory (330).  A wait costs the issuing thread some 200 cycles more
-// while MMAs are in flight, so there
-// are two issuers, and the tokens' arrival counts on the unpacked tile's barrier.
+// scale is applied once per group outside.  With A in TMEM a K = 16 MMA takes about 120
+// cycles however few the tokens, so a stage's eight take some 950; measured are 0.63 us a
+// stage (1200 cycles) with groups of 128, 0.9 with 64 and 1.5 with 32, whose sums bound it.
+// Its codes would take 330 cycles from memory.  A wait costs the issuing thread some 200
+// cycles more while MMAs are in flight, so there are two issuers, and the tokens' arrival
+// counts on the unpacked tile's barrier.
 // ---------------------------------------------------------------------------
 constexpr int QW_THREADS = 640;
 constexpr int QW_ROWS = 128, QW_TOK = 96, QW_COLS = 128;

@@ -146,7 +146,7 @@ int launch_quant_wide(const CUtensorMap &mC, const CUtensorMap &mX, QuantWideArg
                            QW_THREADS, QW_SMEM, st, mC, mX, a);
 }
 
-// y = x w^T for more than 16 tokens.
+// y = x w^T for any number of tokens, on tcgen05.
 int linear_quant_wide(const void *x, const void *q, const void *s, int N, int M, int K, int G, void *y,
                       DeviceInfo *info, cudaStream_t st) {
     QuantWideArgs a = {};
