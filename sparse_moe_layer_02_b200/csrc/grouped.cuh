@@ -544,17 +544,22 @@ __global__ void __launch_bounds__(GrpCfg<MODE>::THREADS, 1)
 // ---------------------------------------------------------------------------
 // fp32: the same three products on the CUDA cores, T x T output tiles, KB summed indices
 // at a time in shared memory, fp32 sums in registers, one running sum each, in index
-// order; the next KB are on their way from memory meanwhile.  The summed index never
-// crosses a segment, so nothing is masked but loads.  Large batches take T = 64 with
-// 8 x 8 sums a thread (four 16-byte shared loads for 64 multiply-adds; with 4 x 4 the
-// shared memory's bandwidth is the bound), small ones T = 32 with 4 x 4: more tiles for
-// the same SMs.
+// order; the next KB (T = 64: the next two, 111 to 86 us for the input gradient of 2048
+// rows, 16 x 768 x 768; T = 32 lost 30 % by it) are on their way from memory meanwhile.  The
+// summed index never crosses a segment, so nothing is masked but loads.  Large batches
+// take T = 64 with 8 x 8 sums a thread (four 16-byte shared loads for 64 multiply-adds;
+// with 4 x 4 the shared memory's bandwidth is the bound), small ones T = 32 with 4 x 4:
+// more tiles for the same SMs.
 // ---------------------------------------------------------------------------
 // Element (k, i) of an operand in shared memory; loads are 16 bytes along the contiguous
 // index: the summed one (KCONT) or the other.
 template <bool KCONT, int T, int KB, int NT> struct F32Operand {
     static constexpr int PER = KB * T / 4 / NT; // pieces of a thread
     float4 v[PER];
+    static constexpr int LD = T == 32 ? T : T + 4;
+    // Where 4 indices i.. of row k lie.  KCONT stores a piece as four scalars of four rows: with
+    // T = 32 the xor spreads a warp's over all banks.
+    static __device__ __forceinline__ int place(int k, int i) { return KCONT && T == 32 ? i ^ (k & 28) : i; }
     // rows: of the contiguous direction's other index; ld: elements from one to the next
     __device__ __forceinline__ void load(const float *p, size_t ld, int nk, int ni, int tid) {
 #pragma unroll
@@ -566,16 +571,17 @@ template <bool KCONT, int T, int KB, int NT> struct F32Operand {
                 v[j] = *reinterpret_cast<const float4 *>(p + (KCONT ? (size_t)i * ld + k : (size_t)k * ld + i));
         }
     }
-    __device__ __forceinline__ void store(float (*s)[T + 4], int tid) const {
+    __device__ __forceinline__ void store(float (*s)[LD], int tid) const {
 #pragma unroll
         for (int j = 0; j < PER; ++j) {
             const int at = tid + j * NT;
             if (KCONT) {
                 const int k = at % (KB / 4) * 4, i = at / (KB / 4);
-                s[k][i] = v[j].x;
-                s[k + 1][i] = v[j].y;
-                s[k + 2][i] = v[j].z;
-                s[k + 3][i] = v[j].w;
+                const int c = place(k, i);
+                s[k][c] = v[j].x;
+                s[k + 1][c] = v[j].y;
+                s[k + 2][c] = v[j].z;
+                s[k + 3][c] = v[j].w;
             } else {
                 *reinterpret_cast<float4 *>(&s[at / (T / 4)][at % (T / 4) * 4]) = v[j];
             }
@@ -583,9 +589,11 @@ template <bool KCONT, int T, int KB, int NT> struct F32Operand {
     }
 };
 
+template <int V> struct IntC { static constexpr int value = V; };
 template <int T> struct GrpF32 {
     static constexpr int SUMS = T == 64 ? 8 : 4; // of a thread, in each direction
     static constexpr int KB = T == 64 ? 16 : 32;
+    static constexpr int AHEAD = T == 64 ? 2 : 1; // blocks of KB on their way
     static constexpr int THREADS = (T / SUMS) * (T / SUMS);
 };
 
@@ -593,7 +601,10 @@ template <int MODE, int T>
 __global__ void __launch_bounds__(GrpF32<T>::THREADS) grouped_f32_kernel(const float *A, const float *B,
                                                                          const GroupedArgs a) {
     constexpr int S = GrpF32<T>::SUMS, NT = GrpF32<T>::THREADS, KB = GrpF32<T>::KB, H = S / 4;
-    __shared__ __align__(16) float sA[KB][T + 4], sB[KB][T + 4];
+    constexpr int AHEAD = GrpF32<T>::AHEAD;
+    using FA = F32Operand<MODE != GRP_WGRAD, T, KB, NT>;
+    using FB = F32Operand<MODE == GRP_FORWARD, T, KB, NT>;
+    __shared__ __align__(16) float sA[KB][FA::LD], sB[KB][FB::LD];
     __shared__ int s_off[GRP_MAXE + 1], s_tile[GRP_MAXE + 1];
     const int tid = threadIdx.x;
     grid_dep_wait(); // all that follows comes after the previous kernel of the stream
@@ -624,34 +635,35 @@ __global__ void __launch_bounds__(GrpF32<T>::THREADS) grouped_f32_kernel(const f
             red = a.red;
         }
         const float *We = B + (size_t)e * a.M * a.K; // forward, dgrad
-        F32Operand<MODE != GRP_WGRAD, T, KB, NT> fa;     // forward x[i][k], dgrad dy[i][k], wgrad dy[r0+k][i]
-        F32Operand<MODE == GRP_FORWARD, T, KB, NT> fb;   // forward W[n][k], dgrad W[k][n], wgrad x[r0+k][n]
-        auto fetch = [&](int k0) {
+        FA fa[AHEAD]; // forward x[i][k], dgrad dy[i][k], wgrad dy[r0+k][i]
+        FB fb[AHEAD]; // forward W[n][k], dgrad W[k][n], wgrad x[r0+k][n]
+        auto fetch = [&](auto slot, int k0) {
+            auto &va = fa[decltype(slot)::value];
+            auto &vb = fb[decltype(slot)::value];
             if (MODE == GRP_WGRAD) {
-                fa.load(A + (size_t)(r0 + k0) * a.M + i0, a.M, red - k0, i1 - i0, tid);
-                fb.load(B + (size_t)(r0 + k0) * a.K + n0, a.K, red - k0, a.ncols - n0, tid);
+                va.load(A + (size_t)(r0 + k0) * a.M + i0, a.M, red - k0, i1 - i0, tid);
+                vb.load(B + (size_t)(r0 + k0) * a.K + n0, a.K, red - k0, a.ncols - n0, tid);
             } else {
-                fa.load(A + (size_t)i0 * a.red + k0, a.red, red - k0, i1 - i0, tid);
+                va.load(A + (size_t)i0 * a.red + k0, a.red, red - k0, i1 - i0, tid);
                 if (MODE == GRP_FORWARD)
-                    fb.load(We + (size_t)n0 * a.K + k0, a.K, red - k0, a.ncols - n0, tid);
+                    vb.load(We + (size_t)n0 * a.K + k0, a.K, red - k0, a.ncols - n0, tid);
                 else
-                    fb.load(We + (size_t)k0 * a.K + n0, a.K, red - k0, a.ncols - n0, tid);
+                    vb.load(We + (size_t)k0 * a.K + n0, a.K, red - k0, a.ncols - n0, tid);
             }
         };
         float acc[S][S] = {};
-        if (red > 0) fetch(0);
-        for (int k0 = 0; k0 < red; k0 += KB) {
-            fa.store(sA, tid);
-            fb.store(sB, tid);
+        auto block = [&](auto slot, int k0) {
+            fa[decltype(slot)::value].store(sA, tid);
+            fb[decltype(slot)::value].store(sB, tid);
             __syncthreads();
-            if (k0 + KB < red) fetch(k0 + KB);
+            if (k0 + AHEAD * KB < red) fetch(slot, k0 + AHEAD * KB);
 #pragma unroll 8
             for (int k = 0; k < KB; ++k) {
                 float xa[S], wb[S];
 #pragma unroll
                 for (int h = 0; h < H; ++h) {
-                    const float4 x = *reinterpret_cast<const float4 *>(&sA[k][h * (T / 2) + ty * 4]);
-                    const float4 w = *reinterpret_cast<const float4 *>(&sB[k][h * (T / 2) + tx * 4]);
+                    const float4 x = *reinterpret_cast<const float4 *>(&sA[k][FA::place(k, h * (T / 2) + ty * 4)]);
+                    const float4 w = *reinterpret_cast<const float4 *>(&sB[k][FB::place(k, h * (T / 2) + tx * 4)]);
                     xa[4 * h] = x.x, xa[4 * h + 1] = x.y, xa[4 * h + 2] = x.z, xa[4 * h + 3] = x.w;
                     wb[4 * h] = w.x, wb[4 * h + 1] = w.y, wb[4 * h + 2] = w.z, wb[4 * h + 3] = w.w;
                 }
@@ -661,6 +673,12 @@ __global__ void __launch_bounds__(GrpF32<T>::THREADS) grouped_f32_kernel(const f
                     for (int n = 0; n < S; ++n) acc[i][n] = fmaf(xa[i], wb[n], acc[i][n]);
             }
             __syncthreads();
+        };
+        if (red > 0) fetch(IntC<0>{}, 0);
+        if (AHEAD > 1 && red > KB) fetch(IntC<AHEAD - 1>{}, KB);
+        for (int k0 = 0; k0 < red; k0 += AHEAD * KB) {
+            block(IntC<0>{}, k0);
+            if (AHEAD > 1 && k0 + KB < red) block(IntC<AHEAD - 1>{}, k0 + KB);
         }
 #pragma unroll
         for (int h = 0; h < H; ++h) {

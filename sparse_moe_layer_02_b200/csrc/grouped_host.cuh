@@ -176,14 +176,18 @@ int grouped_impl(const void *A, const void *B, const int32_t *offsets, int rows,
 
     if (dtype == MOE_F32) {
         // 64 x 64 tiles need less shared memory traffic, 32 x 32 tiles spread few rows over
-        // the SMs (us, 32 / 64): forward, 256 rows, 16 x 256 x 256 9.7 / 18.7; 1024 rows,
-        // 8 x 512 x 512 (128 tiles of 64) 28 / 37; 1500 rows, 20 x 512 x 900 (190 tiles)
-        // 93 / 104, its dgrad (345) 107 / 84; 4000 rows, 8 x 1024 x 1024 368 / 231.  wgrad,
-        // whose tiles do not depend on the rows: 4 x 256 x 256 (64) 3.6 / 3.7,
-        // 16 x 256 x 256 (256) 5.9 / 4.1, 16 x 512 x 512 26 / 16.
-        const size_t large = MODE == GRP_WGRAD ? (size_t)E * ((M + 63) / 64) * ((K + 63) / 64)
-                                               : (size_t)rows * ncols / (64 * 64);
-        const bool small = 2 * large < (MODE == GRP_WGRAD ? 1 : 3) * (size_t)dev->sms;
+        // the SMs and fill better where experts have few (us, 32 / 64): forward, 256 rows,
+        // 16 x 256 x 256 8.9 / 18.1; 1024 rows, 8 x 512 x 512 (128 tiles of 64) 23 / 36; 2000
+        // rows, 8 x 1024 x 512 (500) 77 / 61; 4000 rows, 8 x 1024 x 1024 290 / 231; 75 rows an
+        // expert: 1500 rows, 20 x 512 x 900 71 / 104, its dgrad 72 / 92; 128 an expert: 2048
+        // rows, 16 x 768 x 768 96 / 88.  wgrad, whose tiles do not depend on the rows:
+        // 4 x 256 x 256 (64 tiles) 3.4 / 3.6, 16 x 256 x 256 (256) 5.7 / 4.2,
+        // 16 x 512 x 512 25 / 16.
+        bool small;
+        if (MODE == GRP_WGRAD)
+            small = (size_t)E * ((M + 63) / 64) * ((K + 63) / 64) * 2 < (size_t)dev->sms;
+        else
+            small = (size_t)rows * ncols / (64 * 64) * 2 < (size_t)dev->sms * 3 || rows < 96 * E;
         const int T = small ? 32 : 64;
         a.nb = (a.ncols + T - 1) / T;
         a.mb = (M + T - 1) / T;

@@ -315,7 +315,6 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], bool fresh, uint32_t a0,
             : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
             : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-template <int V> struct IntC { static constexpr int value = V; };
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t v, uint32_t c) {
     const __nv_bfloat162 o = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&v),
                                      *reinterpret_cast<const __nv_bfloat162 *>(&c));
