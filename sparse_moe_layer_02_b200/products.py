@@ -136,16 +136,17 @@ def _differentiable(x, W, offsets):
     it was made on.  A backward pass captured on another stream would have to join that
     stream, which ends the capture and the process.  So every call leaves its stream on the
     nodes (which its own pass now holds), and a captured one reads it first."""
-    leaves = [t for t in (x, W) if t.requires_grad and t.is_leaf]
-    here = torch.cuda.current_stream().cuda_stream
+    leaves = [t.requires_grad and t.is_leaf for t in (x, W)]
+    here = _current_stream(torch.cuda.current_device())
     if torch.cuda.is_current_stream_capturing():
-        for t in leaves:
-            if _accumulation(t).get("moe_stream", here) != here:
+        for t, leaf in zip((x, W), leaves):
+            if leaf and _accumulation(t).get("moe_stream", here) != here:
                 raise ValueError("capturing: an eager pass over the same leaf tensors, made on another "
                                  "stream, is still alive; drop its outputs first")
     y = _GroupedLinear.apply(x, W, offsets)
-    for t in leaves:
-        _accumulation(t).setdefault("moe_stream", here)
+    for leaf, (node, _) in zip(leaves, y.grad_fn.next_functions):
+        if leaf:
+            node.metadata.setdefault("moe_stream", here)
     return y
 
 
@@ -159,7 +160,10 @@ def moe_grouped_linear(x, W, offsets, y=None, stream=None):
     if torch.is_grad_enabled() and (x.requires_grad or W.requires_grad):
         if y is not None or stream is not None:
             raise ValueError("y and stream: not with gradients (use torch.no_grad, torch.cuda.stream)")
-        with torch.cuda.device(_device(x, W, offsets)):
+        dev = _device(x, W, offsets)
+        if dev == torch.cuda.current_device():
+            return _differentiable(x, W, offsets)
+        with torch.cuda.device(dev):
             return _differentiable(x, W, offsets)
     return _linear(x, W, offsets, y, stream)
 
