@@ -78,8 +78,8 @@ __global__ void __launch_bounds__(QZ_THREADS) quantize_kernel(const __nv_bfloat1
             asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(sf));
 #pragma unroll
             for (int j = 7; j >= 0; --j) {
-                const float u = fmaf(w[j], r, 3072.0f);                      // 3072 + a multiple of 2^-12
-                const uint32_t n = __float_as_uint(u + (12582920.0f - 3072.0f)); // 0x4B400000 + code
+                const float u = fmaf(w[j], r, 0x1.8p11f);                     // 1.5 * 2^11 + a multiple of 2^-12
+                const uint32_t n = __float_as_uint(u + (12582920.0f - 0x1.8p11f)); // 0x4B400000 + code
                 c = c * 16u + (n - 0x4B400000u);
             }
         } else {
