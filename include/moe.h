@@ -238,6 +238,9 @@ int moe_version(void);
  *     (the decode down kernel's shared tiles, or the prefill combine kernel)
  *     waits for one more expert tile than exists, so the wait runs out, the
  *     status word reports MOE_ERR_DEVICE_TIMEOUT and the kernel returns normally.
+ *     In the bf16 products grouped by expert and the products with 4-bit weights
+ *     (moe_forward_quant's included), every block with work waits for a signal
+ *     that is never given; their outputs are unspecified then.
  */
 int moe_debug_set_wait_limit_ns(uint64_t ns);
 int moe_debug_never_signal(int on);

@@ -99,6 +99,19 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, uint64
     }
 }
 
+// Waits (10 ms at most each) for the copies of the last stages that a producer issued, out
+// of `issued` in a ring of `ring` places, so that none is under way when the block's shared
+// memory goes away.  A producer calls it however its loop ended: it may have issued its
+// last stages and then a wait of another warp ran out, after which nobody waits for them.
+// Only the issuer's arrivals and the copies' bytes may complete `full`; where every stage
+// was consumed the waits return at once.
+__device__ __forceinline__ void drain_copies(uint64_t *full, uint32_t ring, uint32_t issued, int where) {
+    for (uint32_t j = issued > ring ? issued - ring : 0; j < issued; ++j) {
+        volatile int no_abort = 0;
+        mbar_wait(&full[j % ring], (j / ring) & 1, 10000000ull, &no_abort, where);
+    }
+}
+
 // ---------------------------------------------------------------------------
 // TMA: 2-D tiled bulk tensor load global -> shared, completion on an mbarrier.
 // c0 is the innermost (contiguous) coordinate in elements, c1 the row.

@@ -225,13 +225,7 @@ __global__ void __launch_bounds__(DEC_THREADS, 1)
                     tma_load_2d(mB, &full[s], sb, kx, c.row0);
                 }
             }
-            if (!ok) {
-                const uint32_t first = it > DEC_STAGES ? it - DEC_STAGES : 0;
-                for (uint32_t j = first; j < it; ++j) {
-                    volatile int no_abort = 0;
-                    mbar_wait(&full[j % DEC_STAGES], (j / DEC_STAGES) & 1, 10000000ull, &no_abort, 201);
-                }
-            }
+            drain_copies(full, DEC_STAGES, it, 201);
         }
         __syncwarp(); // lanes 1-31 wait here for lane 0: the warp reconverges
     } else if (warp == 1) {

@@ -598,14 +598,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
                     }
                 }
             }
-            if (!ok) {
-                // Let copies already issued land before the CTA's memory goes away.
-                const uint32_t first = it > GEMM_STAGES ? it - GEMM_STAGES : 0;
-                for (uint32_t j = first; j < it; ++j) {
-                    volatile int no_abort = 0;
-                    mbar_wait(&full[j % GEMM_STAGES], (j / GEMM_STAGES) & 1, 10000000ull, &no_abort, 101);
-                }
-            }
+            drain_copies(full, GEMM_STAGES, it, 101);
         }
         __syncwarp(); // lanes 1-31 wait here for lane 0: the warp reconverges
     } else if (warp == 1) {
@@ -878,14 +871,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
                     tma_load_2d_pair(mB, fb, sa + PAIR_A_BYTES, kx, brow);
                 }
             }
-            if (!ok && rank == 0) {
-                // Let copies already issued land before the pair's memory goes away.
-                const uint32_t first = it > PAIR_STAGES ? it - PAIR_STAGES : 0;
-                for (uint32_t j = first; j < it; ++j) {
-                    volatile int no_abort = 0;
-                    mbar_wait(&full[j % PAIR_STAGES], (j / PAIR_STAGES) & 1, 10000000ull, &no_abort, 141);
-                }
-            }
+            if (rank == 0) drain_copies(full, PAIR_STAGES, it, 141); // both CTAs' copies
         }
         __syncwarp();
     } else if (warp == 1) {
@@ -956,6 +942,13 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
     }
 
     if (KIND == GEMM_DOWN && warp >= 2 && lane == 0) bulk_wait_group<0>(); // stores done
+    // After a wait that ran out, CTA 0 may have announced fewer stages than CTA 1 issued;
+    // those copies count on no barrier that CTA 1 could read, so they get a millisecond.
+    if (rank == 1 && *abort_flag) {
+        const uint64_t t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < 1000000ull) __nanosleep(1000);
+    }
+    __syncwarp();
     tc_fence_before();
     // Neither CTA leaves while the pair's MMAs may still read its shared memory or
     // the other CTA may still arrive on its barriers.

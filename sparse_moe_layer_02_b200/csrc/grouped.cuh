@@ -64,6 +64,7 @@ struct GroupedArgs {
     void *out;
     int zero_rest; // forward, dgrad: write zeros to the rows of no expert
     int split;    // blocks of a cluster that share a tile's k-blocks
+    int never_signal; // test hook: the MMA warp first waits for what never comes
     uint64_t wait_limit_ns;
 };
 
@@ -343,14 +344,7 @@ __global__ void __launch_bounds__(GrpCfg<MODE>::THREADS, 1)
                     }
                 }
             }
-            if (!ok) {
-                // Let copies already issued land before the CTA's memory goes away.
-                const uint32_t first = it > GRP_STAGES ? it - GRP_STAGES : 0;
-                for (uint32_t j = first; j < it; ++j) {
-                    volatile int no_abort = 0;
-                    mbar_wait(&full[j % GRP_STAGES], (j / GRP_STAGES) & 1, 10000000ull, &no_abort, 302);
-                }
-            }
+            drain_copies(full, GRP_STAGES, it, 302);
         }
         __syncwarp();
     } else if (warp == 1) {
@@ -359,6 +353,10 @@ __global__ void __launch_bounds__(GrpCfg<MODE>::THREADS, 1)
         // lane 0 waits and issues.
         uint32_t it = 0, tc = 0;
         bool ok = true;
+        if (a.never_signal && tile0 < total) {
+            if (lane == 0) ok = mbar_wait(drain, 0, limit, abort_flag, 310);
+            ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+        }
         for (int t = tile0; t < total && ok; t += step) {
             const GroupedTile c = grouped_tile<MODE>(t, a, s_off, s_tile);
             const int i0 = c.kb * rank / split, i1 = c.kb * (rank + 1) / split;

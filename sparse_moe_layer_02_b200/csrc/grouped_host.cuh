@@ -173,6 +173,7 @@ int grouped_impl(const void *A, const void *B, const int32_t *offsets, int rows,
     a.out = out;
     a.zero_rest = zero_rest ? 1 : 0;
     a.wait_limit_ns = g_wait_limit_ns;
+    a.never_signal = g_never_signal;
 
     if (dtype == MOE_F32) {
         // 64 x 64 tiles need less shared memory traffic, 32 x 32 tiles spread few rows over

@@ -220,7 +220,7 @@ template <int RG, int MT, int KW, int NT, int G> struct QmCfg {
     static constexpr int FIT = (ROOM - 1024 - RED_BYTES - JOIN_BYTES - TAB_BYTES) / STAGE;
     static constexpr int STAGES = FIT < 12 ? FIT : 12;
     static constexpr int SMEM = 1024 + STAGES * STAGE + RED_BYTES + JOIN_BYTES + TAB_BYTES;
-    static_assert(STAGES >= 2 && (3 * STAGES + 2) * 8 + 4 <= 384, "ring depth");
+    static_assert(STAGES >= 2 && (3 * STAGES + 2) * 8 + 8 <= 384, "ring depth");
 };
 
 struct QuantArgs {
@@ -240,6 +240,7 @@ struct QuantArgs {
     void *out;   // LINEAR y bf16; GATE_UP h bf16; DOWN slot fp32
     void *out_s; // GATE_UP h_sh bf16; DOWN osh fp32
     float gate_max, up_max;
+    int never_signal; // test hook: the shaper first waits for what never comes
     uint64_t wait_limit_ns;
 };
 
@@ -349,6 +350,7 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<RG, MT, KW, NT, G>::BLOCKS)
     uint64_t *empty = full + C::STAGES, *raw = empty + C::STAGES;
     uint64_t *jfull = raw + C::STAGES, *jempty = jfull + 1;
     volatile int *abort_flag = reinterpret_cast<volatile int *>(jempty + 1);
+    int *shaped = reinterpret_cast<int *>(jempty + 1) + 1; // stages that the shaper has arrived for
     int *s_tile = reinterpret_cast<int *>(reinterpret_cast<uint8_t *>(full) + 384);
     int *s_cnt = s_tile + QM_MAXE + 1;
 
@@ -413,6 +415,8 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<RG, MT, KW, NT, G>::BLOCKS)
         grid_dep_wait();
         grid_dep_launch_dependents();
     }
+
+    uint32_t issued = 0, fetched = 0; // stages of tokens and of weights (the producer's)
 
     if (warp == 8) {
         // ------------------------------ producer ------------------------------
@@ -481,15 +485,8 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<RG, MT, KW, NT, G>::BLOCKS)
                 }
             }
         }
-        if (!ok && lane == 0) {
-            // Let copies already issued land before the block's memory goes away.
-            const uint32_t last = it > ahead ? it : ahead;
-            for (uint32_t j = last > C::STAGES ? last - C::STAGES : 0; j < last; ++j) {
-                volatile int no_abort = 0;
-                if (j < it) mbar_wait(&raw[j % C::STAGES], (j / C::STAGES) & 1, 10000000ull, &no_abort, 402);
-                mbar_wait(&full[j % C::STAGES], (j / C::STAGES) & 1, 10000000ull, &no_abort, 403);
-            }
-        }
+        issued = it;
+        fetched = it > ahead ? it : ahead;
     } else if (warp == 9) {
         // ------------------------------ shaper ------------------------------
         // Brings the tokens of a stage, in place, into the order and scale of the MMA's
@@ -497,69 +494,74 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<RG, MT, KW, NT, G>::BLOCKS)
         // over each unit of columns that shares a scale within a slice.
         constexpr int LANES = C::UNIT / 8; // neighbouring lanes that hold one unit of a token
         uint32_t s = 0, ph = 0;
-        for (int t = tile0; t < total; t += step) {
+        int done = 0; // stages shaped
+        bool ok = true;
+        if (a.never_signal && tile0 < total)
+            ok = __all_sync(0xffffffffu, mbar_wait(jfull, 0, limit, abort_flag, 404));
+        for (int t = tile0; t < total && ok; t += step) {
             QuantTile c;
             if (!quant_tile<KIND, TT>(t, routed, a, s_tile, s_cnt, c)) continue;
             const int turns = (c.cnt * C::PIECES + 31) / 32;
             const int K = c.shared ? a.K_s : a.K, stages = (K + SK - 1) / SK;
             for (int i = stages * rank / split; i < stages * (rank + 1) / split; ++i) {
-                bool ok = mbar_wait(&raw[s], ph, limit, abort_flag, 405);
+                ok = mbar_wait(&raw[s], ph, limit, abort_flag, 405);
                 ok = __all_sync(0xffffffffu, ok);
-                if (ok) {
-                    uint8_t *xs = ring_x + s * C::X_BYTES;
-                    float *us = reinterpret_cast<float *>(ring_u + s * C::U_BYTES);
-                    // B turns of 32 pieces from turn j0 on (those past the tokens shape what
-                    // nobody reads); columns past K become zeros.
-                    auto shape = [&](auto count, int j0) {
-                        constexpr int B = decltype(count)::value;
-                        uint4 v[B], *p[B];
-                        float sum[B];
+                if (!ok) break; // and no arrival: the others' waits end by the abort flag
+                uint8_t *xs = ring_x + s * C::X_BYTES;
+                float *us = reinterpret_cast<float *>(ring_u + s * C::U_BYTES);
+                // B turns of 32 pieces from turn j0 on (those past the tokens shape what
+                // nobody reads); columns past K become zeros.
+                auto shape = [&](auto count, int j0) {
+                    constexpr int B = decltype(count)::value;
+                    uint4 v[B], *p[B];
+                    float sum[B];
 #pragma unroll
-                        for (int j = 0; j < B; ++j) {
-                            const int at = (j0 + j) * 32 + lane, piece = at % C::PIECES;
-                            p[j] = reinterpret_cast<uint4 *>(xs + at / C::PIECES * C::XLD + piece * 16);
-                            v[j] = i * SK + piece * 8 < K ? *p[j] : make_uint4(0u, 0u, 0u, 0u);
-                        }
-#pragma unroll
-                        for (int j = 0; j < B; ++j) {
-                            float f[8];
-                            unpack_bf16x2(v[j].x, f[0], f[1]);
-                            unpack_bf16x2(v[j].y, f[2], f[3]);
-                            unpack_bf16x2(v[j].z, f[4], f[5]);
-                            unpack_bf16x2(v[j].w, f[6], f[7]);
-                            sum[j] = ((f[0] + f[1]) + (f[2] + f[3])) + ((f[4] + f[5]) + (f[6] + f[7]));
-                            *p[j] = make_uint4(mul_bf16x2(__byte_perm(v[j].x, v[j].z, 0x5410), QM_X_LO),
-                                               mul_bf16x2(__byte_perm(v[j].x, v[j].z, 0x7632), QM_X_HI),
-                                               mul_bf16x2(__byte_perm(v[j].y, v[j].w, 0x5410), QM_X_LO),
-                                               mul_bf16x2(__byte_perm(v[j].y, v[j].w, 0x7632), QM_X_HI));
-                        }
-#pragma unroll
-                        for (int d = 1; d < LANES; d <<= 1)
-#pragma unroll
-                            for (int j = 0; j < B; ++j) sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], d);
-#pragma unroll
-                        for (int j = 0; j < B; ++j) {
-                            const int at = (j0 + j) * 32 + lane;
-                            if (lane % LANES == 0)
-                                us[at % C::PIECES / LANES * TT + at / C::PIECES] = sum[j] * QM_OFF;
-                        }
-                    };
-                    if (turns == 1) {
-                        shape(IntC<1>{}, 0);
-                    } else {
-                        constexpr int B = C::TURNS < 4 ? C::TURNS : 4;
-#pragma unroll 1
-                        for (int j0 = 0; j0 < turns; j0 += B) shape(IntC<B>{}, j0);
+                    for (int j = 0; j < B; ++j) {
+                        const int at = (j0 + j) * 32 + lane, piece = at % C::PIECES;
+                        p[j] = reinterpret_cast<uint4 *>(xs + at / C::PIECES * C::XLD + piece * 16);
+                        v[j] = i * SK + piece * 8 < K ? *p[j] : make_uint4(0u, 0u, 0u, 0u);
                     }
-                    __syncwarp();
+#pragma unroll
+                    for (int j = 0; j < B; ++j) {
+                        float f[8];
+                        unpack_bf16x2(v[j].x, f[0], f[1]);
+                        unpack_bf16x2(v[j].y, f[2], f[3]);
+                        unpack_bf16x2(v[j].z, f[4], f[5]);
+                        unpack_bf16x2(v[j].w, f[6], f[7]);
+                        sum[j] = ((f[0] + f[1]) + (f[2] + f[3])) + ((f[4] + f[5]) + (f[6] + f[7]));
+                        *p[j] = make_uint4(mul_bf16x2(__byte_perm(v[j].x, v[j].z, 0x5410), QM_X_LO),
+                                           mul_bf16x2(__byte_perm(v[j].x, v[j].z, 0x7632), QM_X_HI),
+                                           mul_bf16x2(__byte_perm(v[j].y, v[j].w, 0x5410), QM_X_LO),
+                                           mul_bf16x2(__byte_perm(v[j].y, v[j].w, 0x7632), QM_X_HI));
+                    }
+#pragma unroll
+                    for (int d = 1; d < LANES; d <<= 1)
+#pragma unroll
+                        for (int j = 0; j < B; ++j) sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], d);
+#pragma unroll
+                    for (int j = 0; j < B; ++j) {
+                        const int at = (j0 + j) * 32 + lane;
+                        if (lane % LANES == 0)
+                            us[at % C::PIECES / LANES * TT + at / C::PIECES] = sum[j] * QM_OFF;
+                    }
+                };
+                if (turns == 1) {
+                    shape(IntC<1>{}, 0);
+                } else {
+                    constexpr int B = C::TURNS < 4 ? C::TURNS : 4;
+#pragma unroll 1
+                    for (int j0 = 0; j0 < turns; j0 += B) shape(IntC<B>{}, j0);
                 }
+                __syncwarp();
                 if (lane == 0) mbar_arrive(&full[s]);
+                ++done;
                 if (++s == C::STAGES) {
                     s = 0;
                     ph ^= 1;
                 }
             }
         }
+        if (lane == 0) *shaped = done;
     } else {
         // ------------------------------ consumers ------------------------------
         const int rg = warp / KS, ks = warp % KS;
@@ -601,12 +603,12 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<RG, MT, KW, NT, G>::BLOCKS)
                 static_cast<float *>(a.out)[at] = v * (a.direct ? a.topk_w[c.row0] : a.w_perm[c.row0 + tk]);
         };
         uint32_t s = 0, ph = 0, jph = 0;
+        bool ok = true; // once false it stays so: no further arrival, but the barriers stay matched
         for (int t = tile0; t < total; t += step) {
             QuantTile c;
             if (!quant_tile<KIND, TT>(t, routed, a, s_tile, s_cnt, c)) continue;
             const int K = c.shared ? a.K_s : a.K;
             const int stages = (K + SK - 1) / SK;
-            bool ok = true;
             // The tile's sums for NTT blocks of 8 tokens (tokens past cnt hold
             // anything: a column of the product depends on its own token only).
             auto sums = [&](auto ntt) {
@@ -624,61 +626,60 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<RG, MT, KW, NT, G>::BLOCKS)
                     on[j] = j * 8 + g < c.cnt;
                 }
 #pragma unroll 1
-                for (int st = stages * rank / split; st < stages * (rank + 1) / split; ++st) {
+                for (int st = ok ? stages * rank / split : stages; st < stages * (rank + 1) / split; ++st) {
                     ok = mbar_wait(&full[s], ph, limit, abort_flag, 411);
                     ok = __all_sync(0xffffffffu, ok);
-                    if (ok) { // else abort: every wait fails at once, the walk stays matched
-                        const uint32_t ws = wbase + s * C::W_BYTES;
-                        const uint8_t *xs = xbase + s * C::X_BYTES, *scs = sbase + s * 2 * C::S_HALF;
-                        const uint8_t *us = ubase + s * C::U_BYTES;
-                        float part[MT][NTT][4];
-                        uint32_t cw[MT][4];
+                    if (!ok) break;
+                    const uint32_t ws = wbase + s * C::W_BYTES;
+                    const uint8_t *xs = xbase + s * C::X_BYTES, *scs = sbase + s * 2 * C::S_HALF;
+                    const uint8_t *us = ubase + s * C::U_BYTES;
+                    float part[MT][NTT][4];
+                    uint32_t cw[MT][4];
 #pragma unroll
-                        for (int b = 0; b < KW / 32; ++b) { // 32 columns each
-                            if (b % 2 == 0) {
+                    for (int b = 0; b < KW / 32; ++b) { // 32 columns each
+                        if (b % 2 == 0) {
 #pragma unroll
-                                for (int i = 0; i < MT; ++i) ldmatrix_x4(ws + woff[b / 2] + i * 8 * C::BOX, cw[i]);
-                            }
+                            for (int i = 0; i < MT; ++i) ldmatrix_x4(ws + woff[b / 2] + i * 8 * C::BOX, cw[i]);
+                        }
 #pragma unroll
-                            for (int j = 0; j < NTT; ++j)
-                                if (on[j])
-                                    xv[j] = *reinterpret_cast<const uint4 *>(xs + j * 8 * C::XLD + b * 64);
+                        for (int j = 0; j < NTT; ++j)
+                            if (on[j])
+                                xv[j] = *reinterpret_cast<const uint4 *>(xs + j * 8 * C::XLD + b * 64);
 #pragma unroll
-                            for (int p = 0; p < 2; ++p)
+                        for (int p = 0; p < 2; ++p)
 #pragma unroll
-                                for (int i = 0; i < MT; ++i) {
-                                    const uint32_t r0 = cw[i][2 * (b % 2)] >> (8 * p);
-                                    const uint32_t r1 = cw[i][2 * (b % 2) + 1] >> (8 * p);
-#pragma unroll
-                                    for (int j = 0; j < NTT; ++j)
-                                        mma_bf16(part[i][j], b % UNIT == 0 && p == 0, r0 & QM_LO, r1 & QM_LO,
-                                                 r0 & QM_HI, r1 & QM_HI, p ? xv[j].z : xv[j].x,
-                                                 p ? xv[j].w : xv[j].y);
-                                }
-                            if ((b + 1) % UNIT == 0) { // the group, or its part here, ends
-                                float2 off[NTT]; // of tokens 2 t4, 2 t4 + 1
+                            for (int i = 0; i < MT; ++i) {
+                                const uint32_t r0 = cw[i][2 * (b % 2)] >> (8 * p);
+                                const uint32_t r1 = cw[i][2 * (b % 2) + 1] >> (8 * p);
 #pragma unroll
                                 for (int j = 0; j < NTT; ++j)
-                                    off[j] = *reinterpret_cast<const float2 *>(us + ((b / UNIT) * TT + j * 8) * 4);
+                                    mma_bf16(part[i][j], b % UNIT == 0 && p == 0, r0 & QM_LO, r1 & QM_LO,
+                                             r0 & QM_HI, r1 & QM_HI, p ? xv[j].z : xv[j].x,
+                                             p ? xv[j].w : xv[j].y);
+                            }
+                        if ((b + 1) % UNIT == 0) { // the group, or its part here, ends
+                            float2 off[NTT]; // of tokens 2 t4, 2 t4 + 1
 #pragma unroll
-                                for (int i = 0; i < MT; ++i) {
-                                    const __nv_bfloat16 *sp =
-                                        reinterpret_cast<const __nv_bfloat16 *>(scs) + (b * 32 / G) * SROW + i * 8;
-                                    const float s0 = __bfloat162float(sp[0]) * QM_UNIT;
-                                    const float s1 = __bfloat162float(sp[SHALF]) * QM_UNIT;
+                            for (int j = 0; j < NTT; ++j)
+                                off[j] = *reinterpret_cast<const float2 *>(us + ((b / UNIT) * TT + j * 8) * 4);
 #pragma unroll
-                                    for (int j = 0; j < NTT; ++j) {
-                                        acc[i][j][0] = fmaf(s0, part[i][j][0] + off[j].x, acc[i][j][0]);
-                                        acc[i][j][1] = fmaf(s0, part[i][j][1] + off[j].y, acc[i][j][1]);
-                                        acc[i][j][2] = fmaf(s1, part[i][j][2] + off[j].x, acc[i][j][2]);
-                                        acc[i][j][3] = fmaf(s1, part[i][j][3] + off[j].y, acc[i][j][3]);
-                                    }
+                            for (int i = 0; i < MT; ++i) {
+                                const __nv_bfloat16 *sp =
+                                    reinterpret_cast<const __nv_bfloat16 *>(scs) + (b * 32 / G) * SROW + i * 8;
+                                const float s0 = __bfloat162float(sp[0]) * QM_UNIT;
+                                const float s1 = __bfloat162float(sp[SHALF]) * QM_UNIT;
+#pragma unroll
+                                for (int j = 0; j < NTT; ++j) {
+                                    acc[i][j][0] = fmaf(s0, part[i][j][0] + off[j].x, acc[i][j][0]);
+                                    acc[i][j][1] = fmaf(s0, part[i][j][1] + off[j].y, acc[i][j][1]);
+                                    acc[i][j][2] = fmaf(s1, part[i][j][2] + off[j].x, acc[i][j][2]);
+                                    acc[i][j][3] = fmaf(s1, part[i][j][3] + off[j].y, acc[i][j][3]);
                                 }
                             }
                         }
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&empty[s]);
                     }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&empty[s]);
                     if (++s == C::STAGES) {
                         s = 0;
                         ph ^= 1;
@@ -773,6 +774,16 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<RG, MT, KW, NT, G>::BLOCKS)
             jph ^= 1;
         }
     }
+    // After a wait that ran out nobody waits for the last copies: let them land before the
+    // block's memory goes away.  All roles have ended, so full lacks just the arrivals that the
+    // shaper did not make.
+    __syncthreads();
+    if (*abort_flag && warp == 8 && lane == 0) {
+        drain_copies(raw, C::STAGES, issued, 402);
+        for (uint32_t j = fetched > C::STAGES ? fetched - C::STAGES : 0; j < fetched; ++j)
+            if ((int)j >= *shaped) mbar_arrive(&full[j % C::STAGES]);
+        drain_copies(full, C::STAGES, fetched, 403);
+    }
     if (split > 1) {
         __syncwarp();
         cluster_sync_all(); // no block leaves while another may still write to it
@@ -864,6 +875,7 @@ struct QuantWideArgs {
     int accs, ld;   // batches of TMEM accumulators; columns of one
     int nb, tts;    // row tiles, token tiles
     int split, own; // blocks of a cluster that share a tile's columns; tokens each finishes
+    int never_signal; // test hook: the MMA issuers first wait for what never comes
     uint64_t wait_limit_ns;
 };
 
@@ -890,6 +902,7 @@ __global__ void __launch_bounds__(QW_THREADS, 1)
     uint64_t *jfull = drain + 2, *jempty = jfull + 1;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(jempty + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    uint32_t *stopped = tmem_slot + 2; // each unpacking warp's first stage without its arrival
     const int warp = warp_id(), lane = lane_id();
 
     if (threadIdx.x == 0) {
@@ -939,6 +952,8 @@ __global__ void __launch_bounds__(QW_THREADS, 1)
     const int gr0 = st0 * GROUPS, groups = min(st1 * GROUPS, a.K / G) - gr0;
     const uint64_t limit = a.wait_limit_ns;
 
+    uint32_t issued = 0; // stages of tokens (their producer's)
+
     if (warp == 0 || warp == 2) {
         if (lane == 0) {
             const bool codes = warp == 0;
@@ -966,14 +981,10 @@ __global__ void __launch_bounds__(QW_THREADS, 1)
                     }
                 }
             }
-            if (!ok) {
-                // Let copies already issued land before the CTA's memory goes away.
-                const uint32_t first = it > ring ? it - ring : 0;
-                for (uint32_t j = first; j < it; ++j) {
-                    volatile int no_abort = 0;
-                    mbar_wait(&full[j % ring], (j / ring) & 1, 10000000ull, &no_abort, 502);
-                }
-            }
+            if (codes)
+                drain_copies(full, ring, it, 502);
+            else
+                issued = it;
         }
         __syncwarp();
     } else if (warp == 1 || warp == 3) {
@@ -981,6 +992,7 @@ __global__ void __launch_bounds__(QW_THREADS, 1)
             const uint32_t turn = warp >> 1;
             uint32_t it = 0, d = 0, ph = 0; // stages so far; accumulators of a batch and their round
             bool ok = true;
+            if (a.never_signal && tile0 < total) ok = mbar_wait(&drain[turn], 0, limit, abort_flag, 511);
             auto next = [&]() {
                 if (++d == (uint32_t)a.accs) {
                     d = 0;
@@ -1083,6 +1095,7 @@ __global__ void __launch_bounds__(QW_THREADS, 1)
                 if (lane == 0) mbar_arrive(&afull[b]);
             }
         }
+        if (lane == 0) stopped[warp - 4] = ok ? UINT32_MAX : it;
     } else {
         const int q = warp & 3; // TMEM lanes 32 q ..: rows q*32 + lane of the tile
         // this warp's tokens of the tile: the first or the second half, in steps of 16
@@ -1189,6 +1202,15 @@ __global__ void __launch_bounds__(QW_THREADS, 1)
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem_base, 512);
+    }
+    // After a wait that ran out nobody waits for the tokens' last copies: let them land before
+    // the block's memory goes away.  All roles have ended, so afull lacks just the arrivals
+    // that the unpacking warps did not make.
+    if (*abort_flag && warp == 2 && lane == 0) {
+        for (uint32_t j = issued > QW_AST ? issued - QW_AST : 0; j < issued; ++j)
+            for (int w = 0; w < QW_UNPACK; ++w)
+                if (stopped[(j & 1) * QW_UNPACK + w] <= j) mbar_arrive(&afull[j % QW_AST]);
+        drain_copies(afull, QW_AST, issued, 502);
     }
     if (SPLIT) {
         __syncwarp();

@@ -162,6 +162,7 @@ int linear_quant_wide(const void *x, const void *q, const void *s, int N, int M,
     a.ld = (a.tok + 31) / 32 * 32;
     a.accs = std::min(QW_UCOL / a.ld, QW_MAXACC) / (G < QW_COLS ? 2 : 1);
     a.wait_limit_ns = g_wait_limit_ns;
+    a.never_signal = g_never_signal;
     CUtensorMap mC, mX;
     auto fn = encode_fn();
     if (!fn) return MOE_ERR_CUDA;
@@ -354,6 +355,7 @@ int moe_linear_quant(const void *x, const void *q, const void *scales, int N, in
     a.ncols = M;
     a.out = y;
     a.wait_limit_ns = g_wait_limit_ns;
+    a.never_signal = g_never_signal;
     // Tiles of 8 tokens, of 16, or the tcgen05 kernel (us).  8 tokens as 16: 2816 x 4096,
     // groups of 64, 9.3 against 8.3; 12288 x 6144 21.7 against 19.6.  16 tokens by tcgen05:
     // 12288 x 6144, groups of 128, 34.6 against 28.2; 24 tokens, groups of 64 in tiles of 16:
@@ -411,6 +413,7 @@ int moe_forward_quant(const void *x, const void *gate_up, const void *gate_up_sc
     a.gate_max = gate_max;
     a.up_max = up_max;
     a.wait_limit_ns = g_wait_limit_ns;
+    a.never_signal = g_never_signal;
     DispatchParams dp = {};
     if (!W.direct) {
         dp.topk_idx = topk_idx;

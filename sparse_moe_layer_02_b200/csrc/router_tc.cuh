@@ -215,13 +215,9 @@ __global__ void __launch_bounds__(RTC_THREADS, 1)
                         tma_load_2d(&mW, &full[s], sa + RTC_A_BYTES + part_i * C::B_PART, kb * RTC_BK,
                                     part_i * E);
             }
-            if (!ok) {
-                const uint32_t first = it > (uint32_t)C::STAGES ? it - C::STAGES : 0;
-                for (uint32_t j = first; j < it; ++j) {
-                    volatile int no_abort = 0;
-                    mbar_wait(&full[j % C::STAGES], (j / C::STAGES) & 1, 10000000ull, &no_abort, 301);
-                }
-            }
+            // (where warps split W_g their arrivals count there too: after one of them has
+            // given up, the limit ends the wait)
+            drain_copies(full, C::STAGES, it, 301);
         }
         __syncwarp(); // lanes 1-31 wait here for lane 0: the warp reconverges
     } else if (warp == 1) {
@@ -253,6 +249,8 @@ __global__ void __launch_bounds__(RTC_THREADS, 1)
                 umma_commit(&empty[s]);
             }
             umma_commit(tfull); // arrives once every MMA issued above has completed
+            volatile int no_abort = 0;
+            mbar_wait(tfull, 0, 100000000ull, &no_abort, 311); // before the ring and TMEM are reused
         }
         __syncwarp();
     } else if (WF32 && !presplit) {
