@@ -335,11 +335,13 @@ int moe_grouped_linear_wgrad(const void *dy, const void *x, const int32_t *offse
  *   prompts: moe_dequantize and then moe_grouped_linear or moe_forward.
  *
  * moe_linear_quant: y = x w^T for tokens x [N, K] bf16, y [N, M] bf16.  The weights
- *   are not rounded to bf16: codes times tokens are summed in fp32 per group, the
- *   scale applied in fp32, y rounded once.  Made for N up to a few hundred; any N
- *   works.  N = 0 is a no-op.  Tokens of magnitude 2^63 and scales of 2^58 and more
- *   may count as infinite (in moe_forward_quant too, the SwiGLU output included); what an
- *   infinite or NaN token or scale gives is infinite or NaN, in its own outputs only.
+ *   are not rounded to bf16: (code - 8) times token is exact, summed in fp32 per group,
+ *   the scale applied in fp32, y rounded once.  So the error goes with sum |x w|, and
+ *   tokens and scales of any finite magnitude are numbers like others, but for sums
+ *   that pass fp32's range (tokens of 2^118 and more may, as part of a group's sum before
+ *   the scale), which count as infinite.  Made for N up to a few hundred; any N works.
+ *   N = 0 is a no-op.  What an infinite or NaN token or scale gives is infinite or NaN,
+ *   in its own outputs only.
  *
  * moe_forward_quant: moe_forward (with moe_forward_clamped's limits; +infinity for
  *   none) on bf16 tokens with every expert in 4 bits: gate_up [E, 2 d_moe, D], gate

@@ -167,17 +167,21 @@ __global__ void __launch_bounds__(QZ_THREADS) dequantize_kernel(const uint8_t *_
 //   (3,7), and the tokens are brought into the same order.
 // - A code is a bf16 as it stands: with exponent bits 0 the bits 0-7 of a bf16 are an
 //   integer times 2^-133 (the lowest normal exponent continues the subnormals), so a
-//   masked code at bits 0-3 is c 2^-133 and one at bits 4-7 is 16 c 2^-133, exactly.
-//   Five logic operations unpack eight codes.  The tokens are scaled by 2^64, or 2^60
-//   against the factor 16, so products lie around 2^-69, far inside fp32; tokens of
-//   2^63 and more become infinite.
-// - The code's offset of 8 is the same for every row: -8 times the group's sum of the
-//   token, which is formed once per stage.
-// - A group's sum is fp32 in the MMA; its scale, with 2^69 on it, is applied once per
-//   group in fp32 (scales of 2^58 and more become infinite).
+//   masked code at bits 0-3 is c 2^-133 and one at bits 4-7 is 16 c 2^-133, exactly.  One
+//   bf16 multiply-add, by 2^127 (2^123) and less 2^-3, makes that (c - 8) / 64, exactly: five
+//   logic operations and four multiply-adds for eight codes.
+// - So the MMA sums centred weights times the tokens as they are: a column coded 8 adds
+//   nothing, whatever its token, and no product of finite tokens leaves fp32's range.
+//   (Summing c and taking 8 times the tokens' sum off per group saves the multiply-adds, but
+//   its error goes with the tokens of columns coded 8 too, and it needs scaled tokens, which
+//   leave fp32's range below 2^-72 and above 2^63.  us, that way / this: a layer of 32 tokens,
+//   D 4096, 128 experts of 1408, 212 / 228; of 64, D 6144, 256 of 2048, groups of 64, 928 / 950
+//   to 985 from run to run; 16 tokens, 12288 x 5120, 24.5 / 21.2, as nobody sums the tokens.)
+// - A group's sum is fp32 in the MMA; its scale is applied once per group in fp32, the
+//   factor 64 once per tile.
 //
-// tcgen05 would want the bf16 weights in shared memory first (four times the codes'
-// bytes written and read again) and has nothing to gain: the tensor work is small here.
+// The tensor work is small here.  With more tokens tcgen05 takes over, its weights unpacked
+// into TMEM (quant_wide_kernel).
 //
 // A block is one producer warp, one shaper warp and eight consumer warps: RG groups of 16 MT
 // rows x KS slices of KW columns (RG * KS = 8).  The producer fills a ring: codes and
@@ -210,8 +214,7 @@ template <int RG, int MT, int KW, int NT, int G> struct QmCfg {
     static constexpr int X_BYTES = NT * 8 * XLD;
     static constexpr int PIECES = SK / 8;               // 16-byte pieces of a token's stage
     static constexpr int TURNS = NT * 8 * PIECES / 32;  // of a warp over all tokens
-    static constexpr int U_BYTES = SK / UNIT * 8 * NT * 4; // the tokens' sums
-    static constexpr int STAGE = W_BYTES + 2 * S_HALF + X_BYTES + U_BYTES;
+    static constexpr int STAGE = W_BYTES + 2 * S_HALF + X_BYTES;
     static constexpr int LD = R + 4; // floats per token in the sums' buffer
     static constexpr int RED_BYTES = KS > 1 ? KS * 8 * NT * LD * 4 : 0;
     static constexpr int JOIN_BYTES = KS > 1 ? 8 * NT * R * 4 : 0; // sums from the blocks of a cluster
@@ -316,15 +319,15 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], bool fresh, uint32_t a0,
             : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
             : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t v, uint32_t c) {
-    const __nv_bfloat162 o = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&v),
-                                     *reinterpret_cast<const __nv_bfloat162 *>(&c));
-    return *reinterpret_cast<const uint32_t *>(&o);
+__device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t d;
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+    return d;
 }
-constexpr uint32_t QM_LO = 0x000F000Fu, QM_HI = 0x00F000F0u;         // codes at bits 0-3, 4-7
-constexpr uint32_t QM_X_LO = 0x5F805F80u, QM_X_HI = 0x5D805D80u;     // 2^64, 2^60 for their tokens
-constexpr float QM_OFF = -0x1p-66f; // -8 times 2^64, in units of 2^-133
-constexpr float QM_UNIT = 0x1p69f;
+constexpr uint32_t QM_LO = 0x000F000Fu, QM_HI = 0x00F000F0u;   // codes at bits 0-3, 4-7
+constexpr uint32_t QM_C_LO = 0x7F007F00u, QM_C_HI = 0x7D007D00u; // 2^127, 2^123: codes / 64
+constexpr uint32_t QM_OFF = 0xBE00BE00u;                       // -8 / 64
+constexpr float QM_UNIT = 64.f;
 
 // Maps: mW codes [E, M, K/2] bytes, box BOX x R x 1, swizzled; mS scales [E, K/G, M], box
 // R x SK/G x 1 (GATE_UP: R/2 rows); the same of the shared expert (GATE_UP: its gate and
@@ -343,8 +346,7 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<RG, MT, KW, NT, G>::BLOCKS)
     uint8_t *ring_w = smem;
     uint8_t *ring_s = ring_w + C::STAGES * C::W_BYTES;
     uint8_t *ring_x = ring_s + C::STAGES * 2 * C::S_HALF;
-    uint8_t *ring_u = ring_x + C::STAGES * C::X_BYTES;
-    float *red = reinterpret_cast<float *>(ring_u + C::STAGES * C::U_BYTES);
+    float *red = reinterpret_cast<float *>(ring_x + C::STAGES * C::X_BYTES);
     float *join = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(red) + C::RED_BYTES);
     uint64_t *full = reinterpret_cast<uint64_t *>(reinterpret_cast<uint8_t *>(join) + C::JOIN_BYTES);
     uint64_t *empty = full + C::STAGES, *raw = empty + C::STAGES;
@@ -489,10 +491,8 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<RG, MT, KW, NT, G>::BLOCKS)
         fetched = it > ahead ? it : ahead;
     } else if (warp == 9) {
         // ------------------------------ shaper ------------------------------
-        // Brings the tokens of a stage, in place, into the order and scale of the MMA's
-        // operand (a lane's 8 columns pair as (0,4), (1,5), (2,6), (3,7)) and sums them
-        // over each unit of columns that shares a scale within a slice.
-        constexpr int LANES = C::UNIT / 8; // neighbouring lanes that hold one unit of a token
+        // Brings the tokens of a stage, in place, into the order of the MMA's operand (a lane's
+        // 8 columns pair as (0,4), (1,5), (2,6), (3,7)), columns past K as zeros.
         uint32_t s = 0, ph = 0;
         int done = 0; // stages shaped
         bool ok = true;
@@ -508,13 +508,11 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<RG, MT, KW, NT, G>::BLOCKS)
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break; // and no arrival: the others' waits end by the abort flag
                 uint8_t *xs = ring_x + s * C::X_BYTES;
-                float *us = reinterpret_cast<float *>(ring_u + s * C::U_BYTES);
                 // B turns of 32 pieces from turn j0 on (those past the tokens shape what
-                // nobody reads); columns past K become zeros.
+                // nobody reads).
                 auto shape = [&](auto count, int j0) {
                     constexpr int B = decltype(count)::value;
                     uint4 v[B], *p[B];
-                    float sum[B];
 #pragma unroll
                     for (int j = 0; j < B; ++j) {
                         const int at = (j0 + j) * 32 + lane, piece = at % C::PIECES;
@@ -522,28 +520,9 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<RG, MT, KW, NT, G>::BLOCKS)
                         v[j] = i * SK + piece * 8 < K ? *p[j] : make_uint4(0u, 0u, 0u, 0u);
                     }
 #pragma unroll
-                    for (int j = 0; j < B; ++j) {
-                        float f[8];
-                        unpack_bf16x2(v[j].x, f[0], f[1]);
-                        unpack_bf16x2(v[j].y, f[2], f[3]);
-                        unpack_bf16x2(v[j].z, f[4], f[5]);
-                        unpack_bf16x2(v[j].w, f[6], f[7]);
-                        sum[j] = ((f[0] + f[1]) + (f[2] + f[3])) + ((f[4] + f[5]) + (f[6] + f[7]));
-                        *p[j] = make_uint4(mul_bf16x2(__byte_perm(v[j].x, v[j].z, 0x5410), QM_X_LO),
-                                           mul_bf16x2(__byte_perm(v[j].x, v[j].z, 0x7632), QM_X_HI),
-                                           mul_bf16x2(__byte_perm(v[j].y, v[j].w, 0x5410), QM_X_LO),
-                                           mul_bf16x2(__byte_perm(v[j].y, v[j].w, 0x7632), QM_X_HI));
-                    }
-#pragma unroll
-                    for (int d = 1; d < LANES; d <<= 1)
-#pragma unroll
-                        for (int j = 0; j < B; ++j) sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], d);
-#pragma unroll
-                    for (int j = 0; j < B; ++j) {
-                        const int at = (j0 + j) * 32 + lane;
-                        if (lane % LANES == 0)
-                            us[at % C::PIECES / LANES * TT + at / C::PIECES] = sum[j] * QM_OFF;
-                    }
+                    for (int j = 0; j < B; ++j)
+                        *p[j] = make_uint4(__byte_perm(v[j].x, v[j].z, 0x5410), __byte_perm(v[j].x, v[j].z, 0x7632),
+                                           __byte_perm(v[j].y, v[j].w, 0x5410), __byte_perm(v[j].y, v[j].w, 0x7632));
                 };
                 if (turns == 1) {
                     shape(IntC<1>{}, 0);
@@ -584,7 +563,6 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<RG, MT, KW, NT, G>::BLOCKS)
         constexpr int SHALF = KIND == QUANT_GATE_UP ? C::S_HALF / 2 : HALF;   // to the second half's
         const uint8_t *sbase = ring_s + ((ks * KW / G) * SROW + rg * 8 * MT + g) * 2;
         const uint8_t *xbase = ring_x + g * C::XLD + ks * KW * 2 + t4 * 16;
-        const uint8_t *ubase = ring_u + (ks * (KW / C::UNIT) * TT + 2 * t4) * 4;
         const int ctid = threadIdx.x;
         // Output (token tk, row of the tile): v, or for GATE_UP gate v and up u.
         auto store = [&](const QuantTile &c, int tk, int row, float v, float u) {
@@ -632,7 +610,6 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<RG, MT, KW, NT, G>::BLOCKS)
                     if (!ok) break;
                     const uint32_t ws = wbase + s * C::W_BYTES;
                     const uint8_t *xs = xbase + s * C::X_BYTES, *scs = sbase + s * 2 * C::S_HALF;
-                    const uint8_t *us = ubase + s * C::U_BYTES;
                     float part[MT][NTT][4];
                     uint32_t cw[MT][4];
 #pragma unroll
@@ -651,29 +628,28 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<RG, MT, KW, NT, G>::BLOCKS)
                             for (int i = 0; i < MT; ++i) {
                                 const uint32_t r0 = cw[i][2 * (b % 2)] >> (8 * p);
                                 const uint32_t r1 = cw[i][2 * (b % 2) + 1] >> (8 * p);
+                                const uint32_t a0 = fma_bf16x2(r0 & QM_LO, QM_C_LO, QM_OFF);
+                                const uint32_t a1 = fma_bf16x2(r1 & QM_LO, QM_C_LO, QM_OFF);
+                                const uint32_t a2 = fma_bf16x2(r0 & QM_HI, QM_C_HI, QM_OFF);
+                                const uint32_t a3 = fma_bf16x2(r1 & QM_HI, QM_C_HI, QM_OFF);
 #pragma unroll
                                 for (int j = 0; j < NTT; ++j)
-                                    mma_bf16(part[i][j], b % UNIT == 0 && p == 0, r0 & QM_LO, r1 & QM_LO,
-                                             r0 & QM_HI, r1 & QM_HI, p ? xv[j].z : xv[j].x,
-                                             p ? xv[j].w : xv[j].y);
+                                    mma_bf16(part[i][j], b % UNIT == 0 && p == 0, a0, a1, a2, a3,
+                                             p ? xv[j].z : xv[j].x, p ? xv[j].w : xv[j].y);
                             }
                         if ((b + 1) % UNIT == 0) { // the group, or its part here, ends
-                            float2 off[NTT]; // of tokens 2 t4, 2 t4 + 1
-#pragma unroll
-                            for (int j = 0; j < NTT; ++j)
-                                off[j] = *reinterpret_cast<const float2 *>(us + ((b / UNIT) * TT + j * 8) * 4);
 #pragma unroll
                             for (int i = 0; i < MT; ++i) {
                                 const __nv_bfloat16 *sp =
                                     reinterpret_cast<const __nv_bfloat16 *>(scs) + (b * 32 / G) * SROW + i * 8;
-                                const float s0 = __bfloat162float(sp[0]) * QM_UNIT;
-                                const float s1 = __bfloat162float(sp[SHALF]) * QM_UNIT;
+                                const float s0 = __bfloat162float(sp[0]);
+                                const float s1 = __bfloat162float(sp[SHALF]);
 #pragma unroll
                                 for (int j = 0; j < NTT; ++j) {
-                                    acc[i][j][0] = fmaf(s0, part[i][j][0] + off[j].x, acc[i][j][0]);
-                                    acc[i][j][1] = fmaf(s0, part[i][j][1] + off[j].y, acc[i][j][1]);
-                                    acc[i][j][2] = fmaf(s1, part[i][j][2] + off[j].x, acc[i][j][2]);
-                                    acc[i][j][3] = fmaf(s1, part[i][j][3] + off[j].y, acc[i][j][3]);
+                                    acc[i][j][0] = fmaf(s0, part[i][j][0], acc[i][j][0]);
+                                    acc[i][j][1] = fmaf(s0, part[i][j][1], acc[i][j][1]);
+                                    acc[i][j][2] = fmaf(s1, part[i][j][2], acc[i][j][2]);
+                                    acc[i][j][3] = fmaf(s1, part[i][j][3], acc[i][j][3]);
                                 }
                             }
                         }
@@ -685,6 +661,12 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<RG, MT, KW, NT, G>::BLOCKS)
                         ph ^= 1;
                     }
                 }
+#pragma unroll
+                for (int i = 0; i < MT; ++i)
+#pragma unroll
+                    for (int j = 0; j < NTT; ++j)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) acc[i][j][r] *= QM_UNIT;
                 if (KS == 1) {
                     if (!ok) return;
 #pragma unroll
