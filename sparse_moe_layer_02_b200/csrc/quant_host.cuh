@@ -42,10 +42,11 @@ bool make_quant_maps(CUtensorMap *mW, CUtensorMap *mS, const void *q, const void
 
 // Blocks that share a tile: as many as still run all at once (clusters do not fill every
 // place, so two thirds of them are counted on), each with two stages of columns at least.
-// A block alone on an SM has too few warps to hide its latencies: 2816 x 4096, one token
-// (22 tiles), takes 9.8 us unshared and 7.2 us shared by 8; 12288 x 6144 (96 tiles) 14.6 us
-// unshared, 15.2 us by 2, 26 us by 8.  Sharing when the tiles already take several rounds
-// costs: the exchange (2 us) then stalls the next tile's reading.
+// A block alone on an SM has too few warps to hide its latencies: one token, groups of 128,
+// 2816 x 4096 (22 tiles) takes 11.2 us unshared, 8.7 shared by 2 and 7.4 by 8; 6144 x 6144 (48)
+// 15.8, 11.5 by 2 and 11.1 by 4; 12288 x 5120 (96) 14.4 and 14.5 by 2 (8 tokens 17.4 and 16.1).
+// Sharing when the tiles already take several rounds costs: the exchange (2 us) then stalls
+// the next tile's reading.
 int quant_split(size_t tiles, size_t slots, int stages) {
     int best = 1;
     for (int c = 2; c <= 8 && tiles * c * 3 <= slots * 2 && stages >= 2 * c; c *= 2) best = c;
@@ -193,11 +194,13 @@ struct QuantWs {
 
 // Tokens of a tile.  Tiles of 8 leave room for more stages of codes, tiles of 16 read an
 // expert's codes once where its tokens are more than 8 (us for the layer, 8 / 16): D 4096,
-// 128 experts of 1408, k 8: 12 tokens 150 / 157, 32 215 / 224, 64 261 / 267, 96 308 / 305,
-// 128 369 / 340; D 4096, 40 of 1024, k 4: 32 tokens 87 / 101, 64 110 / 116, 96 150 / 142, 512
-// 501 / 403.  The shared expert's codes are read again by every tile of tokens: D 6144,
-// 256 of 2048, k 8, 128 tokens (four an expert) 1035 / 1016.  (Tiles of 32 leave one block an
-// SM and were slower everywhere: the first at 512 tokens 1182, against 893.)
+// 128 experts of 1408, k 8: 12 tokens 155 / 161, 32 227 / 234, 64 276 / 280, 96 334 / 309,
+// 128 401 / 339; D 4096, 40 of 1024, k 4: 32 tokens 86 / 96, 48 (4.8 an expert) 100 / 100, 64
+// 107 / 104, 96 149 / 123.  The shared expert's codes are read again by every tile of tokens:
+// D 6144, 256 of 2048, k 8, groups of 64: 64 tokens 960 / 984, 96 (three an expert) 1110 /
+// 1105, 128 1218 / 1205.  (Small layers, with fewer tiles than places, would gain from 8 for
+// longer: D 1024, 8 of 512, k 2: 64 tokens 20 / 22, 100 26 / 24.)  Tiles of 32 leave one block
+// an SM and were slower everywhere: the first at 512 tokens 1182, against 893.
 int quant_tile_tokens(int N, int k, int E) {
     return N <= 8 || (N <= 64 && (size_t)N * k <= (size_t)4 * E) ? 8 : 16;
 }
@@ -356,15 +359,21 @@ int moe_linear_quant(const void *x, const void *q, const void *scales, int N, in
     a.out = y;
     a.wait_limit_ns = g_wait_limit_ns;
     a.never_signal = g_never_signal;
-    // Tiles of 8 tokens, of 16, or the tcgen05 kernel (us).  8 tokens as 16: 2816 x 4096,
-    // groups of 64, 9.3 against 8.3; 12288 x 6144 21.7 against 19.6.  16 tokens by tcgen05:
-    // 12288 x 6144, groups of 128, 34.6 against 28.2; 24 tokens, groups of 64 in tiles of 16:
-    // 2816 x 4096 14.1 against 12.0, 6144 x 6144 28.6 against 28.3, 12288 x 5120 37.9 against
-    // 34.2; 64 tokens there 66.6 against 39.3.  Groups of 32 make four sums of a stage there:
-    // 24 tokens, 12288 x 5120, 61 against 44 in tiles of 16; 48 tokens 59 against 44; 64
-    // tokens 67 against 72.
-    if (N <= 8) return linear_quant_t<4, 2, 128, 1>(q, scales, a, dev, st);
-    if (N <= 16 || (group == 32 && N <= 48)) return linear_quant_t<4, 2, 128, 2>(q, scales, a, dev, st);
+    // Tiles of 8 tokens, of 16, or the tcgen05 kernel, whose sums cost more the more groups a
+    // stage has (us, in this order; G the group, - not measured):
+    //   8 tokens   12288 x 5120, G 64 16.4 / 16.9 / 31.0   28672 x 4096, G 64 20.8 / 21.4 / 49.5
+    //   16         12288 x 5120, G 128 23.3 / 21.2 / 29.2  28672 x 4096, G 128 36.8 / 26.6 / 44.6
+    //   24         12288 x 5120, G 128 23.5 / 30.7 / 29.5  28672 x 4096, G 128 48.2 / 48.6 / 45.1
+    //              12288 x 5120, G 64 23.9 / 31.7 / 35.0   2816 x 4096, G 64 10.8 / 11.9 / 12.1
+    //              12288 x 5120, G 32 25.3 / 35.6 / 62.7   2816 x 4096, G 32 11.0 / 13.1 / 16.5
+    //   32         12288 x 5120, G 128 39.5 / 30.8 / 29.7  2816 x 4096, G 128 13.6 / 11.8 / 11.5
+    //              12288 x 5120, G 64 40.6 / 31.9 / 35.3   2816 x 4096, G 64 13.7 / 12.1 / 12.2
+    //   48         12288 x 5120, G 64 44.4 / 32.0 / 36.1   2816 x 4096, G 64 14.4 / 14.3 / 12.8
+    //              28672 x 4096, G 64 86.8 / 67.8 / 57.2
+    //              12288 x 5120, G 32 47.2 / 35.4 / 60.4   2816 x 4096, G 32 14.8 / 15.0 / 17.2
+    //   64         12288 x 5120, G 32 - / 60.5 / 68.9      2816 x 4096, G 32 - / 20.2 / 18.7
+    if (N <= 8 || (N > 16 && N <= 24)) return linear_quant_t<4, 2, 128, 1>(q, scales, a, dev, st);
+    if (N <= (group == 32 ? 48 : group == 64 ? 32 : 16)) return linear_quant_t<4, 2, 128, 2>(q, scales, a, dev, st);
     return linear_quant_wide(x, q, scales, N, M, K, group, y, dev, st);
 }
 
@@ -451,10 +460,11 @@ int moe_forward_quant(const void *x, const void *gate_up, const void *gate_up_sc
     const QuantLayer w = {gate_up, gate_up_scales, down, down_scales, sh_gate_up, sh_gate_up_scales,
                           sh_down, sh_down_scales, D, d_moe, d_sh};
     // Tiles of 256 weight rows cost least per row (a row's sum stays in one warp, and the
-    // tokens are laid out half as often), those of 128 are more even where there are few:
-    // 4 tokens, D 4096, 128 experts of 1408 (about 320 tiles of 256 rows for 296 places):
-    // 82 us against 74; 8 tokens, D 6144, 256 experts of 2048 (1040 tiles): gate and up
-    // rows 152 us against 171.  The tiles are estimated, as the routing is on the device.
+    // tokens are laid out half as often), those of 128 are more even where there are few (us
+    // for the layer, 256 / 128): D 4096, 128 experts of 1408: one token 35 / 30, 4 (about 360
+    // tiles of 256 rows for 296 places) 84 / 76, 8 (715) 115 / 119, 32 227 / 246; D 6144, 256 of
+    // 2048, groups of 64: 4 tokens (530) 153 / 151, 8 (1040) 253 / 246, 32 650 / 676.  The tiles
+    // are estimated, as the routing is on the device.
     const size_t tt = std::max<size_t>(std::min<size_t>((size_t)N * k, E), (size_t)N * k / W.tile_rows) +
                       (N + W.tile_rows - 1) / W.tile_rows;
     const bool few = tt * ((d_moe + 127) / 128) < (size_t)dev->sms * 4;

@@ -1,5 +1,5 @@
 """The products with 4-bit weights over the range of their tokens and codes, for token counts on
-both sides of the kernels' choice (8 and 16, 48 with groups of 32, to one; 17 and more to the other).
+both sides of the choices between kernels and tiles.
 
 Tolerances.  (code - 8) * token is exact in fp32 (4 + 8 bits).  A tensor-core step of 16 products
 is taken to lose at most 2^-22 of its largest partial sum, and a group's multiply-add and the
@@ -40,7 +40,7 @@ def _check(got, x, w):
 
 
 @pytest.mark.parametrize("G", [32, 64, 128])
-@pytest.mark.parametrize("N", [1, 8, 16, 17, 50])
+@pytest.mark.parametrize("N", [1, 8, 16, 17, 24, 25, 33, 50])
 def test_tokens_and_scales_of_any_size(N, G):
     g = _gen(N + G)
     q, s = moe.moe_quantize(_randn(g, 264, 1024, std=0.02), G)
@@ -54,7 +54,7 @@ def test_tokens_and_scales_of_any_size(N, G):
 
 
 @pytest.mark.parametrize("G", [32, 64, 128])
-@pytest.mark.parametrize("N", [8, 16, 17, 50])
+@pytest.mark.parametrize("N", [8, 16, 17, 25, 33, 50])
 def test_tokens_below_the_normal_numbers(N, G):
     """Tokens around 2^-126 with large scales: nothing is flushed to zero on the way."""
     g = _gen(N + G)
@@ -66,7 +66,7 @@ def test_tokens_below_the_normal_numbers(N, G):
 
 
 @pytest.mark.parametrize("G", [32, 64, 128])
-@pytest.mark.parametrize("N", [1, 8, 16, 17, 50])
+@pytest.mark.parametrize("N", [1, 8, 16, 17, 24, 25, 33, 50])
 def test_columns_coded_zero_leave_no_residue(N, G):
     """Rows with one weight other than 0, on columns of small tokens; large tokens elsewhere."""
     g = _gen(3 * N + G)

@@ -59,7 +59,8 @@ CASES = {
     "grouped_many": lambda: _grouped([600] * 24, 1024, 128),      # tiles of two stages, several a block
     "linear_1": lambda: _linear(1, 1024, 4096, 64),
     "linear_16": lambda: _linear(16, 40000, 256, 32),             # short sums, more tiles than places
-    "linear_20": lambda: _linear(20, 1024, 4096, 64),             # shared by clusters
+    "linear_20": lambda: _linear(20, 1024, 4096, 64),
+    "linear_40": lambda: _linear(40, 1024, 4096, 64),             # shared by clusters
     "linear_97": lambda: _linear(97, 20480, 256, 32),             # two stages a tile
     "layer_1": lambda: _layer(1, 512, 6, 2, 512, 64),
     "layer_5": lambda: _layer(5, 512, 6, 2, 512, 64),
