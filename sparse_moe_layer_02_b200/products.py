@@ -130,19 +130,22 @@ def _accumulation(leaf):
 
 def _differentiable(x, W, offsets):
     """_GroupedLinear, refusing a capture on a leaf whose gradient accumulation belongs to an
-    eager pass.
+    eager pass on the default stream.
 
-    Autograd keeps one accumulation node per leaf while any pass holds it, tied to the stream
-    it was made on.  A backward pass captured on another stream would have to join that
-    stream, which ends the capture and the process.  So every call leaves its stream on the
-    nodes (which its own pass now holds), and a captured one reads it first."""
+    Autograd keeps one accumulation node per leaf while any pass (or a wrapper, such as a
+    data-parallel one) holds it, tied to the stream it was made on.  A backward pass captured
+    on another stream joins that stream: one that can be captured takes part, the default
+    stream (handle 0) cannot, which ends the capture and the process.  So every call leaves
+    its stream on the nodes it is the first to see, and a captured one reads it.  A node that
+    something else made on the default stream, and that a call on another stream saw first,
+    is not recognised."""
     leaves = [t.requires_grad and t.is_leaf for t in (x, W)]
     here = _current_stream(torch.cuda.current_device())
     if torch.cuda.is_current_stream_capturing():
         for t, leaf in zip((x, W), leaves):
-            if leaf and _accumulation(t).get("moe_stream", here) != here:
-                raise ValueError("capturing: an eager pass over the same leaf tensors, made on another "
-                                 "stream, is still alive; drop its outputs first")
+            if leaf and _accumulation(t).get("moe_stream", here) == 0:
+                raise ValueError("capturing: an eager pass over the same leaf tensors, made on the default "
+                                 "stream, is still alive; drop its outputs first, or run it on another stream")
     y = _GroupedLinear.apply(x, W, offsets)
     for leaf, (node, _) in zip(leaves, y.grad_fn.next_functions):
         if leaf:
