@@ -18,13 +18,18 @@
  *     moe_device_status() reads.
  *   - Pointers must be 16-byte aligned.  For bf16 tensors the row lengths D,
  *     d_moe and d_sh must be multiples of 8 (16-byte rows for TMA).
+ *   - Calls run in the calling thread's current context and leave it current.  A
+ *     thread that has none gets the current device's primary context.
+ *     A process uses one context per device: the kernels' attributes are set in
+ *     the first, and calls in another may return MOE_ERR_CUDA.
  *   - Calls on one device may overlap only if they are on one stream: the
  *     kernels share nothing across calls except the status word, but two
  *     moe_forward calls must not share a workspace while both are in flight.
  *   - Stream order is kept.  Some kernels use programmatic dependent launch
- *     (the tensor-core router, the decode gate_up kernel).  They may be resident
- *     before the previous work on the stream ends, but they touch no memory until
- *     it has completed.  Kernels of this library also release their own
+ *     (the tensor-core router, the decode gate_up kernel, the products by expert
+ *     and with 4-bit weights).  They may be resident before the previous work on
+ *     the stream ends, but they touch no memory until the work before the call has
+ *     completed.  Kernels of this library also release their own
  *     successors early (griddepcontrol.launch_dependents).  So a caller's kernel
  *     launched right after with programmatic stream serialization must wait for
  *     its predecessor (griddepcontrol.wait / cudaGridDependencySynchronize)

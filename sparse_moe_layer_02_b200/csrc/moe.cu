@@ -83,13 +83,27 @@ struct DeviceInfo {
 DeviceInfo g_dev[kMaxDevices];
 std::mutex g_mu;
 
+bool context_is_current() {
+    static PFN_cuCtxGetCurrent_v4000 fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPoint("cuCtxGetCurrent", &p, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<PFN_cuCtxGetCurrent_v4000>(p);
+    });
+    CUcontext ctx = nullptr;
+    return fn && fn(&ctx) == CUDA_SUCCESS && ctx;
+}
+
 int current_device_info(DeviceInfo **out) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return MOE_ERR_CUDA;
-    // Binds the device's context to this thread: a thread that has made no CUDA call
-    // yet (autograd's backward thread) has none, and the tensor maps' driver call
-    // needs one.
-    if (cudaSetDevice(dev) != cudaSuccess) return MOE_ERR_CUDA;
+    // A thread that has made no CUDA call yet (autograd's backward thread) has no context,
+    // and the tensor maps' driver call needs one: the device's own is bound then.  A context
+    // that is current stays, one that the caller made with the driver's interface too.
+    if (!context_is_current() && cudaSetDevice(dev) != cudaSuccess) return MOE_ERR_CUDA;
     std::lock_guard<std::mutex> lk(g_mu);
     DeviceInfo &d = g_dev[dev];
     if (!d.ready) {
