@@ -240,6 +240,13 @@ bool quant_layer_shape_ok(int N, int D, int E, int d, int d_sh, int k, int G) {
            quant_shape_ok(1, 2 * d_sh, D, G) && quant_shape_ok(1, D, d_sh, G);
 }
 
+// A layer that moe_forward_quant takes, with its plan; tile numbers are 32-bit.
+bool quant_layer_ok(int N, int D, int E, int d, int d_sh, int k, int G, QuantWs &W) {
+    return quant_layer_shape_ok(N, D, E, d, d_sh, k, G) && plan_quant(N, D, E, d, d_sh, k, W) &&
+           (W.rows_max / 8 + 1) * ((size_t)std::max(D, std::max(d, d_sh)) / 32 + 1) +
+                   ((size_t)N / 8 + 1) * ((size_t)std::max(D, d_sh) / 16 + 1) <= (size_t)INT32_MAX / 2;
+}
+
 struct QuantLayer {
     const void *gu, *gu_s, *dn, *dn_s, *sgu, *sgu_s, *sdn, *sdn_s;
     int D, d, d_sh;
@@ -378,9 +385,8 @@ int moe_linear_quant(const void *x, const void *q, const void *scales, int N, in
 }
 
 size_t moe_forward_quant_workspace(int N, int D, int E, int d_moe, int d_sh, int k) {
-    if (N < 0 || D <= 0 || E <= 0 || E > DISPATCH_MAXE || d_moe <= 0 || d_sh <= 0 || k <= 0 || k > 32) return 0;
     QuantWs W;
-    return plan_quant(N, D, E, d_moe, d_sh, k, W) ? W.total : 0;
+    return quant_layer_ok(N, D, E, d_moe, d_sh, k, 32, W) ? W.total : 0; // what any group allows, 32 does
 }
 
 int moe_forward_quant(const void *x, const void *gate_up, const void *gate_up_scales, const void *down,
@@ -391,11 +397,7 @@ int moe_forward_quant(const void *x, const void *gate_up, const void *gate_up_sc
                       void *stream) {
     if (gate_max != gate_max || up_max != up_max || up_max < 0.f) return MOE_ERR_ARG;
     QuantWs W;
-    if (!quant_layer_shape_ok(N, D, E, d_moe, d_sh, k, group) || !plan_quant(N, D, E, d_moe, d_sh, k, W))
-        return MOE_ERR_SHAPE;
-    if ((W.rows_max / 8 + 1) * ((size_t)std::max(D, std::max(d_moe, d_sh)) / 32 + 1) +
-            ((size_t)N / 8 + 1) * ((size_t)std::max(D, d_sh) / 16 + 1) > (size_t)INT32_MAX / 2)
-        return MOE_ERR_SHAPE; // tile numbers are 32-bit
+    if (!quant_layer_ok(N, D, E, d_moe, d_sh, k, group, W)) return MOE_ERR_SHAPE;
     if (N == 0) return MOE_OK;
     for (const void *p : {x, gate_up, gate_up_scales, down, down_scales, sh_gate_up, sh_gate_up_scales,
                           sh_down, sh_down_scales, (const void *)topk_idx, (const void *)topk_w,
