@@ -88,7 +88,9 @@ def _same_type(*ts):
             raise ValueError("the tensors must share one dtype")
 
 
-def _check_offsets(offsets, E):
+def _check_sizes(rows, offsets, E):
+    if rows > 0x7FFFFFFF:  # an int's, in the library
+        raise ValueError("at most 2^31 - 1 rows")
     if offsets.dtype != torch.int32 or tuple(offsets.shape) != (E + 1,):
         raise ValueError("offsets must be int32 [E + 1]")
 
@@ -99,7 +101,7 @@ def _linear(x, W, offsets, y, stream):
     dev = _device(x, W, offsets)
     _same_type(x, W)
     (rows, K), (E, M, _) = x.shape, W.shape
-    _check_offsets(offsets, E)
+    _check_sizes(rows, offsets, E)
     rest = int(y is None)
     y = _out(y, (rows, M), x.dtype, x, "y", stream)
     _call("moe_grouped_linear", dev, stream, x.data_ptr(), W.data_ptr(), offsets.data_ptr(), rows,
@@ -179,7 +181,7 @@ def moe_grouped_linear_dgrad(dy, W, offsets, dx=None, stream=None):
     dev = _device(dy, W, offsets)
     _same_type(dy, W)
     rows, (E, M, K) = dy.shape[0], W.shape
-    _check_offsets(offsets, E)
+    _check_sizes(rows, offsets, E)
     rest = int(dx is None)
     dx = _out(dx, (rows, K), dy.dtype, dy, "dx", stream)
     _call("moe_grouped_linear_dgrad", dev, stream, dy.data_ptr(), W.data_ptr(), offsets.data_ptr(),
@@ -195,7 +197,7 @@ def moe_grouped_linear_wgrad(dy, x, offsets, dW=None, stream=None):
     dev = _device(dy, x, offsets)
     _same_type(dy, x)
     (rows, M), K, E = dy.shape, x.shape[1], offsets.shape[0] - 1
-    _check_offsets(offsets, E)
+    _check_sizes(rows, offsets, E)
     dW = _out(dW, (E, M, K), dy.dtype, dy, "dW", stream)
     _call("moe_grouped_linear_wgrad", dev, stream, dy.data_ptr(), x.data_ptr(), offsets.data_ptr(),
           rows, E, M, K, _dt(dy), dW.data_ptr())

@@ -1,5 +1,9 @@
 """Host-side refusals of the products by expert and of the 4-bit layer (no GPU)."""
 
+import pytest
+import torch
+from torch._subclasses.fake_tensor import FakeTensorMode
+
 import sparse_moe_layer_02_b200 as moe
 
 
@@ -21,3 +25,15 @@ def test_no_workspace_for_a_layer_that_is_refused():
     for good in (dict(), dict(D=32, d=32, d_sh=32), dict(N=0), dict(N=1), dict(N=100000, D=6144, E=256, d=2048)):
         w, refused = both(**good)
         assert w > 0 and not refused, good
+
+
+@pytest.mark.parametrize("rows", [2 ** 31, 2 ** 32 + 5])
+def test_more_rows_than_an_int_counts_are_refused(rows):
+    """Tensors without memory: the library's argument would wrap (2^32 + 5 rows to 5)."""
+    with FakeTensorMode():
+        t = lambda *s, dtype=torch.bfloat16: torch.empty(s, dtype=dtype, device="cuda")
+        x, W, off, dy = t(rows, 8), t(2, 16, 8), t(3, dtype=torch.int32), t(rows, 16)
+        for f in (lambda: moe.moe_grouped_linear(x, W, off), lambda: moe.moe_grouped_linear_dgrad(dy, W, off),
+                  lambda: moe.moe_grouped_linear_wgrad(dy, x, off)):
+            with pytest.raises(ValueError, match="rows"):
+                f()
