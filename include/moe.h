@@ -358,6 +358,7 @@ int moe_grouped_linear_wgrad(const void *dy, const void *x, const int32_t *offse
  *   and y is rounded once.  Results are bitwise reproducible.
  *   workspace: moe_forward_quant_workspace() bytes (0 for invalid sizes), 256-byte
  *   aligned; not shared by calls in flight at once, captured graphs included.
+ * Outputs and the workspace must not overlap inputs.
  * Errors: MOE_ERR_SHAPE, MOE_ERR_ARG, MOE_ERR_WORKSPACE.
  */
 int moe_quantize(const void *W, int E, int M, int K, int group, void *q, void *scales, void *stream);

@@ -565,6 +565,10 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<RG, MT, KW, NT, G>::BLOCKS)
         const uint8_t *xbase = ring_x + g * C::XLD + ks * KW * 2 + t4 * 16;
         const int ctid = threadIdx.x;
         // Output (token tk, row of the tile): v, or for GATE_UP gate v and up u.
+        // The SwiGLU output is rounded to bf16, as in the fused forward: it is the down product's
+        // MMA operand, whose type is the tokens'.  In two bf16 parts it would double that product's
+        // MMAs and its tokens' bytes; as it is, the layer lies 2.3e-3 from fp64 (row norm), against
+        // 1.7e-3 with an fp32 h.  The other sums stay in fp32 up to y.
         auto store = [&](const QuantTile &c, int tk, int row, float v, float u) {
             const int nc = c.shared ? a.ncols_s : a.ncols;
             const int col = c.nb * (KIND == QUANT_GATE_UP ? HALF : R) + row;
