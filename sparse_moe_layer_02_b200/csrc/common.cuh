@@ -99,17 +99,25 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, uint64
     }
 }
 
-// Waits (10 ms at most each) for the copies of the last stages that a producer issued, out
-// of `issued` in a ring of `ring` places, so that none is under way when the block's shared
-// memory goes away.  A producer calls it however its loop ended: it may have issued its
-// last stages and then a wait of another warp ran out, after which nobody waits for them.
-// Only the issuer's arrivals and the copies' bytes may complete `full`; where every stage
-// was consumed the waits return at once.
-__device__ __forceinline__ void drain_copies(uint64_t *full, uint32_t ring, uint32_t issued, int where) {
-    for (uint32_t j = issued > ring ? issued - ring : 0; j < issued; ++j) {
-        volatile int no_abort = 0;
-        mbar_wait(&full[j % ring], (j / ring) & 1, 10000000ull, &no_abort, where);
-    }
+// Wait for what this block has under way (copies, MMAs) to end.  In an ordinary call a wait like
+// others, with their limit; once that has run out, or another wait of the block, for grace_ns
+// more: what is under way ends by itself, and nobody else waits for it then.
+__device__ __forceinline__ void settle(uint64_t *bar, uint32_t parity, uint64_t limit_ns,
+                                       volatile int *abort_flag, uint64_t grace_ns, int where) {
+    if (mbar_wait(bar, parity, limit_ns, abort_flag, where)) return;
+    volatile int no_abort = 0;
+    mbar_wait(bar, parity, grace_ns, &no_abort, where);
+}
+
+// Settles the copies of the last stages that a producer issued, out of `issued` in a ring of
+// `ring` places, so that none is under way when the block's shared memory goes away.  A
+// producer calls it however its loop ended: it may have issued its last stages and then a wait
+// of another warp ran out.  Only the issuer's arrivals and the copies' bytes may complete
+// `full`; where every stage was consumed the waits return at once.
+__device__ __forceinline__ void drain_copies(uint64_t *full, uint32_t ring, uint32_t issued, uint64_t limit_ns,
+                                             volatile int *abort_flag, int where) {
+    for (uint32_t j = issued > ring ? issued - ring : 0; j < issued; ++j)
+        settle(&full[j % ring], (j / ring) & 1, limit_ns, abort_flag, 10000000ull, where);
 }
 
 // ---------------------------------------------------------------------------

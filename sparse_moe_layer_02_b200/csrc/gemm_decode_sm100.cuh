@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(DEC_THREADS, 1)
                     tma_load_2d(mB, &full[s], sb, kx, c.row0);
                 }
             }
-            drain_copies(full, DEC_STAGES, it, 201);
+            drain_copies(full, DEC_STAGES, it, limit, abort_flag, 201);
         }
         __syncwarp(); // lanes 1-31 wait here for lane 0: the warp reconverges
     } else if (warp == 1) {
@@ -257,8 +257,7 @@ __global__ void __launch_bounds__(DEC_THREADS, 1)
                 umma_commit(&tfull[acc]);
             }
             umma_commit(drain);
-            volatile int no_abort = 0;
-            mbar_wait(drain, 0, 100000000ull, &no_abort, 212);
+            settle(drain, 0, limit, abort_flag, 100000000ull, 212);
         }
         __syncwarp();
     } else {

@@ -598,7 +598,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
                     }
                 }
             }
-            drain_copies(full, GEMM_STAGES, it, 101);
+            drain_copies(full, GEMM_STAGES, it, limit, abort_flag, 101);
         }
         __syncwarp(); // lanes 1-31 wait here for lane 0: the warp reconverges
     } else if (warp == 1) {
@@ -631,8 +631,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
             }
             // Drain: wait until every MMA issued by this thread has completed.
             umma_commit(drain);
-            volatile int no_abort = 0;
-            mbar_wait(drain, 0, 100000000ull, &no_abort, 112);
+            settle(drain, 0, limit, abort_flag, 100000000ull, 112);
         }
         __syncwarp();
     } else {
@@ -871,7 +870,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
                     tma_load_2d_pair(mB, fb, sa + PAIR_A_BYTES, kx, brow);
                 }
             }
-            if (rank == 0) drain_copies(full, PAIR_STAGES, it, 141); // both CTAs' copies
+            if (rank == 0) drain_copies(full, PAIR_STAGES, it, limit, abort_flag, 141); // both CTAs' copies
         }
         __syncwarp();
     } else if (warp == 1) {
@@ -904,8 +903,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
             }
             // Drain: wait until every MMA issued by this thread has completed.
             umma_commit_pair(drain);
-            volatile int no_abort = 0;
-            mbar_wait(drain, 0, 100000000ull, &no_abort, 152);
+            settle(drain, 0, limit, abort_flag, 100000000ull, 152);
         }
         __syncwarp();
     } else {

@@ -344,7 +344,7 @@ __global__ void __launch_bounds__(GrpCfg<MODE>::THREADS, 1)
                     }
                 }
             }
-            drain_copies(full, GRP_STAGES, it, 302);
+            drain_copies(full, GRP_STAGES, it, limit, abort_flag, 302);
         }
         __syncwarp();
     } else if (warp == 1) {
@@ -416,8 +416,7 @@ __global__ void __launch_bounds__(GrpCfg<MODE>::THREADS, 1)
         if (lane == 0) {
             // Drain: wait until every MMA issued by this thread has completed.
             umma_commit(drain);
-            volatile int no_abort = 0;
-            mbar_wait(drain, 0, 100000000ull, &no_abort, 313);
+            settle(drain, 0, limit, abort_flag, 100000000ull, 313);
         }
         __syncwarp();
     } else if (SPLIT) {

@@ -765,10 +765,10 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<RG, MT, KW, NT, G>::BLOCKS)
     // shaper did not make.
     __syncthreads();
     if (*abort_flag && warp == 8 && lane == 0) {
-        drain_copies(raw, C::STAGES, issued, 402);
+        drain_copies(raw, C::STAGES, issued, limit, abort_flag, 402);
         for (uint32_t j = fetched > C::STAGES ? fetched - C::STAGES : 0; j < fetched; ++j)
             if ((int)j >= *shaped) mbar_arrive(&full[j % C::STAGES]);
-        drain_copies(full, C::STAGES, fetched, 403);
+        drain_copies(full, C::STAGES, fetched, limit, abort_flag, 403);
     }
     if (split > 1) {
         __syncwarp();
@@ -968,7 +968,7 @@ __global__ void __launch_bounds__(QW_THREADS, 1)
                 }
             }
             if (codes)
-                drain_copies(full, ring, it, 502);
+                drain_copies(full, ring, it, limit, abort_flag, 502);
             else
                 issued = it;
         }
@@ -1028,8 +1028,7 @@ __global__ void __launch_bounds__(QW_THREADS, 1)
             }
             // Drain: wait until every MMA issued by this thread has completed.
             umma_commit(&drain[turn]);
-            volatile int no_abort = 0;
-            mbar_wait(&drain[turn], 0, 100000000ull, &no_abort, 515);
+            settle(&drain[turn], 0, limit, abort_flag, 100000000ull, 515);
         }
         __syncwarp();
     } else if (warp >= 4 && warp < 12) {
@@ -1196,7 +1195,7 @@ __global__ void __launch_bounds__(QW_THREADS, 1)
         for (uint32_t j = issued > QW_AST ? issued - QW_AST : 0; j < issued; ++j)
             for (int w = 0; w < QW_UNPACK; ++w)
                 if (stopped[(j & 1) * QW_UNPACK + w] <= j) mbar_arrive(&afull[j % QW_AST]);
-        drain_copies(afull, QW_AST, issued, 502);
+        drain_copies(afull, QW_AST, issued, limit, abort_flag, 502);
     }
     if (SPLIT) {
         __syncwarp();

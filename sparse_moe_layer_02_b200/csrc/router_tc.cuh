@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(RTC_THREADS, 1)
             }
             // (where warps split W_g their arrivals count there too: after one of them has
             // given up, the limit ends the wait)
-            drain_copies(full, C::STAGES, it, 301);
+            drain_copies(full, C::STAGES, it, limit, abort_flag, 301);
         }
         __syncwarp(); // lanes 1-31 wait here for lane 0: the warp reconverges
     } else if (warp == 1) {
@@ -249,8 +249,7 @@ __global__ void __launch_bounds__(RTC_THREADS, 1)
                 umma_commit(&empty[s]);
             }
             umma_commit(tfull); // arrives once every MMA issued above has completed
-            volatile int no_abort = 0;
-            mbar_wait(tfull, 0, 100000000ull, &no_abort, 311); // before the ring and TMEM are reused
+            settle(tfull, 0, limit, abort_flag, 100000000ull, 311); // before the ring and TMEM are reused
         }
         __syncwarp();
     } else if (WF32 && !presplit) {
