@@ -168,15 +168,15 @@ __global__ void __launch_bounds__(QZ_THREADS) dequantize_kernel(const uint8_t *_
 // - A code is a bf16 as it stands: with exponent bits 0 the bits 0-7 of a bf16 are an
 //   integer times 2^-133 (the lowest normal exponent continues the subnormals), so a
 //   masked code at bits 0-3 is c 2^-133 and one at bits 4-7 is 16 c 2^-133, exactly.  One
-//   bf16 multiply-add, by 2^127 (2^123) and less 2^-3, makes that (c - 8) / 64, exactly: five
-//   logic operations and four multiply-adds for eight codes.
+//   bf16 multiply-add, by 2^127 (2^123) and less 2^-3, makes that (c - 8) / 64, exactly: four
+//   logic operations and five multiply-adds for eight codes (centred_codes).
 // - So the MMA sums centred weights times the tokens as they are: a column coded 8 adds
 //   nothing, whatever its token, and no product of finite tokens leaves fp32's range.
 //   (Summing c and taking 8 times the tokens' sum off per group saves the multiply-adds, but
 //   its error goes with the tokens of columns coded 8 too, and it needs scaled tokens, which
 //   leave fp32's range below 2^-72 and above 2^63.  us, that way / this: a layer of 32 tokens,
-//   D 4096, 128 experts of 1408, 212 / 228; of 64, D 6144, 256 of 2048, groups of 64, 928 / 950
-//   to 985 from run to run; 16 tokens, 12288 x 5120, 24.5 / 21.2, as nobody sums the tokens.)
+//   D 4096, 128 experts of 1408, 211 / 220; of 64, D 6144, 256 of 2048, groups of 64, 904 / 882;
+//   16 tokens, 12288 x 6144, 27.4 / 23.6, as nobody sums the tokens.)
 // - A group's sum is fp32 in the MMA; its scale is applied once per group in fp32, the
 //   factor 64 once per tile.
 //
@@ -328,6 +328,18 @@ constexpr uint32_t QM_LO = 0x000F000Fu, QM_HI = 0x00F000F0u;   // codes at bits 
 constexpr uint32_t QM_C_LO = 0x7F007F00u, QM_C_HI = 0x7D007D00u; // 2^127, 2^123: codes / 64
 constexpr uint32_t QM_OFF = 0xBE00BE00u;                       // -8 / 64
 constexpr float QM_UNIT = 64.f;
+// (code - 8) / 64 for the codes at bits 0-3 (lo) and 4-7 (hi) of each half of a word, or with
+// p = 1 at bits 8-11 and 12-15.  These come down to bits 0-7 by bytes, which leaves nothing above
+// them, so the low code is the byte less the high one, by a multiply-add in place of a mask:
+// logic operations have half the rate (a layer of 32 tokens, D 4096, 128 experts of 1408: 220 us;
+// with a shift and two masks 228).
+__device__ __forceinline__ void centred_codes(uint32_t w, int p, uint32_t &lo, uint32_t &hi) {
+    const uint32_t r = p ? __byte_perm(w, 0u, 0x4341) : w;
+    const uint32_t h = r & QM_HI;
+    hi = fma_bf16x2(h, QM_C_HI, QM_OFF);
+    lo = p ? fma_bf16x2(r, QM_C_LO, fma_bf16x2(h, QM_C_LO ^ 0x80008000u, QM_OFF))
+           : fma_bf16x2(r & QM_LO, QM_C_LO, QM_OFF);
+}
 
 // Maps: mW codes [E, M, K/2] bytes, box BOX x R x 1, swizzled; mS scales [E, K/G, M], box
 // R x SK/G x 1 (GATE_UP: R/2 rows); the same of the shared expert (GATE_UP: its gate and
@@ -630,12 +642,9 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<RG, MT, KW, NT, G>::BLOCKS)
                         for (int p = 0; p < 2; ++p)
 #pragma unroll
                             for (int i = 0; i < MT; ++i) {
-                                const uint32_t r0 = cw[i][2 * (b % 2)] >> (8 * p);
-                                const uint32_t r1 = cw[i][2 * (b % 2) + 1] >> (8 * p);
-                                const uint32_t a0 = fma_bf16x2(r0 & QM_LO, QM_C_LO, QM_OFF);
-                                const uint32_t a1 = fma_bf16x2(r1 & QM_LO, QM_C_LO, QM_OFF);
-                                const uint32_t a2 = fma_bf16x2(r0 & QM_HI, QM_C_HI, QM_OFF);
-                                const uint32_t a3 = fma_bf16x2(r1 & QM_HI, QM_C_HI, QM_OFF);
+                                uint32_t a0, a1, a2, a3;
+                                centred_codes(cw[i][2 * (b % 2)], p, a0, a2);
+                                centred_codes(cw[i][2 * (b % 2) + 1], p, a1, a3);
 #pragma unroll
                                 for (int j = 0; j < NTT; ++j)
                                     mma_bf16(part[i][j], b % UNIT == 0 && p == 0, a0, a1, a2, a3,

@@ -43,8 +43,8 @@ bool make_quant_maps(CUtensorMap *mW, CUtensorMap *mS, const void *q, const void
 // Blocks that share a tile: as many as still run all at once (clusters do not fill every
 // place, so two thirds of them are counted on), each with two stages of columns at least.
 // A block alone on an SM has too few warps to hide its latencies: one token, groups of 128,
-// 2816 x 4096 (22 tiles) takes 11.2 us unshared, 8.7 shared by 2 and 7.4 by 8; 6144 x 6144 (48)
-// 15.8, 11.5 by 2 and 11.1 by 4; 12288 x 5120 (96) 14.4 and 14.5 by 2 (8 tokens 17.4 and 16.1).
+// 2816 x 4096 (22 tiles) takes 11.0 us unshared, 8.6 shared by 2 and 7.4 by 8; 6144 x 6144 (48)
+// 15.5, 11.4 by 2 and 10.9 by 4; 12288 x 5120 (96) 14.1 and 14.3 by 2 (8 tokens 17.0 and 15.7).
 // Sharing when the tiles already take several rounds costs: the exchange (2 us) then stalls
 // the next tile's reading.
 int quant_split(size_t tiles, size_t slots, int stages) {
@@ -194,13 +194,13 @@ struct QuantWs {
 
 // Tokens of a tile.  Tiles of 8 leave room for more stages of codes, tiles of 16 read an
 // expert's codes once where its tokens are more than 8 (us for the layer, 8 / 16): D 4096,
-// 128 experts of 1408, k 8: 12 tokens 155 / 161, 32 227 / 234, 64 276 / 280, 96 334 / 309,
-// 128 401 / 339; D 4096, 40 of 1024, k 4: 32 tokens 86 / 96, 48 (4.8 an expert) 100 / 100, 64
-// 107 / 104, 96 149 / 123.  The shared expert's codes are read again by every tile of tokens:
-// D 6144, 256 of 2048, k 8, groups of 64: 64 tokens 960 / 984, 96 (three an expert) 1110 /
-// 1105, 128 1218 / 1205.  (Small layers, with fewer tiles than places, would gain from 8 for
-// longer: D 1024, 8 of 512, k 2: 64 tokens 20 / 22, 100 26 / 24.)  Tiles of 32 leave one block
-// an SM and were slower everywhere: the first at 512 tokens 1182, against 893.
+// 128 experts of 1408, k 8: 12 tokens 149 / 157, 32 219 / 229, 64 265 / 272, 96 319 / 301,
+// 128 387 / 334; D 4096, 40 of 1024, k 4: 32 tokens 89 / 95, 48 (4.8 an expert) 97 / 98, 64
+// 103 / 101 to 107, 96 142 / 123.  The shared expert's codes are read again by every tile of
+// tokens: D 6144, 256 of 2048, k 8, groups of 64, 128 tokens (four an expert) 1146 / 1088.
+// (Small layers, with fewer tiles than places, would gain from 8 for longer: D 1024, 8 of 512,
+// k 2: 64 tokens 20 / 22, 100 26 / 24.)  Tiles of 32 leave one block an SM and were slower
+// everywhere: the first at 512 tokens 1182, against 893.
 int quant_tile_tokens(int N, int k, int E) {
     return N <= 8 || (N <= 64 && (size_t)N * k <= (size_t)4 * E) ? 8 : 16;
 }
@@ -368,17 +368,17 @@ int moe_linear_quant(const void *x, const void *q, const void *scales, int N, in
     a.never_signal = g_never_signal;
     // Tiles of 8 tokens, of 16, or the tcgen05 kernel, whose sums cost more the more groups a
     // stage has (us, in this order; G the group, - not measured):
-    //   8 tokens   12288 x 5120, G 64 16.4 / 16.9 / 31.0   28672 x 4096, G 64 20.8 / 21.4 / 49.5
-    //   16         12288 x 5120, G 128 23.3 / 21.2 / 29.2  28672 x 4096, G 128 36.8 / 26.6 / 44.6
-    //   24         12288 x 5120, G 128 23.5 / 30.7 / 29.5  28672 x 4096, G 128 48.2 / 48.6 / 45.1
-    //              12288 x 5120, G 64 23.9 / 31.7 / 35.0   2816 x 4096, G 64 10.8 / 11.9 / 12.1
-    //              12288 x 5120, G 32 25.3 / 35.6 / 62.7   2816 x 4096, G 32 11.0 / 13.1 / 16.5
-    //   32         12288 x 5120, G 128 39.5 / 30.8 / 29.7  2816 x 4096, G 128 13.6 / 11.8 / 11.5
-    //              12288 x 5120, G 64 40.6 / 31.9 / 35.3   2816 x 4096, G 64 13.7 / 12.1 / 12.2
-    //   48         12288 x 5120, G 64 44.4 / 32.0 / 36.1   2816 x 4096, G 64 14.4 / 14.3 / 12.8
-    //              28672 x 4096, G 64 86.8 / 67.8 / 57.2
-    //              12288 x 5120, G 32 47.2 / 35.4 / 60.4   2816 x 4096, G 32 14.8 / 15.0 / 17.2
-    //   64         12288 x 5120, G 32 - / 60.5 / 68.9      2816 x 4096, G 32 - / 20.2 / 18.7
+    //   8 tokens   12288 x 5120, G 64 16.3 / 16.5 / 30.9   28672 x 4096, G 64 20.3 / 20.6 / 49.1
+    //   16         12288 x 5120, G 128 22.3 / 20.9 / 29.1  28672 x 4096, G 128 35.0 / 25.8 / 44.6
+    //   24         12288 x 5120, G 128 22.5 / 29.7 / 29.4  28672 x 4096, G 128 46.5 / 47.4 / 45.2
+    //              12288 x 5120, G 64 23.4 / 31.1 / 34.9   2816 x 4096, G 64 10.7 / 11.8 / 12.1
+    //              12288 x 5120, G 32 25.1 / 35.2 / 62.4   2816 x 4096, G 32 10.8 / 12.9 / 16.5
+    //   32         12288 x 5120, G 128 38.2 / 29.8 / 29.6  2816 x 4096, G 128 13.3 / 11.7 / 11.5
+    //              12288 x 5120, G 64 39.6 / 31.3 / 35.0   2816 x 4096, G 64 13.5 / 12.0 / 12.2
+    //   48         12288 x 5120, G 64 43.3 / 31.4 / 35.9   2816 x 4096, G 64 14.0 / 14.2 / 12.8
+    //              28672 x 4096, G 64 84.7 / 66.8 / 57.2
+    //              12288 x 5120, G 32 47.0 / 35.3 / 60.4   2816 x 4096, G 32 14.3 / 14.9 / 17.2
+    //   64         12288 x 5120, G 32 - / 59.5 / 68.8      2816 x 4096, G 32 - / 20.0 / 18.7
     if (N <= 8 || (N > 16 && N <= 24)) return linear_quant_t<4, 2, 128, 1>(q, scales, a, dev, st);
     if (N <= (group == 32 ? 48 : group == 64 ? 32 : 16)) return linear_quant_t<4, 2, 128, 2>(q, scales, a, dev, st);
     return linear_quant_wide(x, q, scales, N, M, K, group, y, dev, st);
@@ -464,8 +464,8 @@ int moe_forward_quant(const void *x, const void *gate_up, const void *gate_up_sc
     // Tiles of 256 weight rows cost least per row (a row's sum stays in one warp, and the
     // tokens are laid out half as often), those of 128 are more even where there are few (us
     // for the layer, 256 / 128): D 4096, 128 experts of 1408: one token 35 / 30, 4 (about 360
-    // tiles of 256 rows for 296 places) 84 / 76, 8 (715) 115 / 119, 32 227 / 246; D 6144, 256 of
-    // 2048, groups of 64: 4 tokens (530) 153 / 151, 8 (1040) 253 / 246, 32 650 / 676.  The tiles
+    // tiles of 256 rows for 296 places) 82 / 74, 8 (715) 111 / 116, 32 219 / 239; D 6144, 256 of
+    // 2048, groups of 64: 4 tokens (530) 150 / 151, 8 (1040) 244 / 246, 32 640 / 680.  The tiles
     // are estimated, as the routing is on the device.
     const size_t tt = std::max<size_t>(std::min<size_t>((size_t)N * k, E), (size_t)N * k / W.tile_rows) +
                       (N + W.tile_rows - 1) / W.tile_rows;
