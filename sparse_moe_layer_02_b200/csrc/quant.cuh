@@ -787,11 +787,11 @@ __global__ void __launch_bounds__(QM_THREADS, QmCfg<RG, MT, KW, NT, G>::BLOCKS)
 
 // ---------------------------------------------------------------------------
 // The product of one matrix with more than 24 tokens (32 with groups of 64, 48 with groups of
-// 32).  There the register kernel's MMA time grows with the tokens (mma.sync m16n8k16, 8 cycles each), so tcgen05 takes over:
-// a tile is 128 weight rows x up to 96 tokens, one block per SM.  Where that leaves SMs
-// idle, the blocks of a cluster share a tile's columns: each sums its own, hands every
-// block its tokens' sums through distributed shared memory, and those are added in the
-// blocks' order.
+// 32).  There the register kernel's MMA time grows with the tokens (mma.sync m16n8k16, 8 cycles
+// each), so tcgen05 takes over: a tile is 128 weight rows x up to 96 tokens, one block per SM.
+// Where that leaves SMs idle, the blocks of a cluster share a tile's columns: each sums its own,
+// hands every block its tokens' sums through distributed shared memory, and those are added in
+// the blocks' order.
 //
 //   warp 0       TMA producer of the codes: 128 columns (8 KiB) a stage
 //   warp 2       TMA producer of the tokens: two swizzled boxes of 64 columns a stage

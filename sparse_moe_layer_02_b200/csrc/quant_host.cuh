@@ -102,8 +102,9 @@ int linear_quant_t(const void *q, const void *s, QuantArgs a, DeviceInfo *info, 
 // Blocks that share a tile of the wide product: its time is that of the tiles one after the
 // other, each its share of the stages (0.6 us each with groups of 128) and what filling the
 // pipeline and joining the sums take, about six stages' time with a cluster and one without
-// (3 rounds of shares by 4 took 35 us where one round unshared took 29.5: 12288 x 5120, 24
-// tokens; 2816 x 4096, 22 row tiles on 148 SMs, took 11.4 shared by 6 and 23.7 unshared).
+// (24 tokens through this kernel: 3 rounds of shares by 4 took 35 us where one round unshared
+// took 29.5 for 12288 x 5120; 2816 x 4096, 22 row tiles on 148 SMs, took 11.4 shared by 6 and
+// 23.7 unshared).
 struct WideSplit {
     int split, grid;
 };
